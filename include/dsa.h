@@ -371,6 +371,136 @@ dsa_status dsa_prefill_layer_noalloc(const dsa_dims* dims, const uint16_t* q,
                                      const float* w_idx, uint16_t* out, float* lse,
                                      int32_t* idx_out, uint32_t* device_status, void* stream);
 
+/* ---- Paged 8-bit latent cache ------------------------------------------
+ *
+ * The cache of many sequences in 8 bits, in pages of a common pool: what a
+ * serving program keeps between steps. A cache row is a token's latent
+ * [d_latent] and its rotary part [d_rope], both as e4m3 codes; row values are
+ * code * scale with one scale for each page (the block of page_size tokens)
+ * and cache head, of which this layer has one: the latent that every query
+ * head shares. Scales are powers of two, so value = code * scale is exact in
+ * bf16 and a code is re-expressed in a grown scale by one rounding.
+ * dsa_cache_append writes rows (with the position rotation), dsa_cache_attn
+ * reads them (causal, or a sliding window and a few first tokens), and
+ * dsa_cache_gather turns a sequence's rows back into the contiguous bf16
+ * latent and rope that dsa_prefill_layer and the other calls take. The pages
+ * describe no paged or 8-bit cache; these are this library's rules.
+ *
+ * Supported: (d_latent, d_rope) in {(512, 64), (64, 16)}, page_size in
+ * {16, 32, 64, 128}, 1 <= n_heads <= 128, max_pages * page_size <= 2^30,
+ * n_tok < 2^24. */
+typedef struct dsa_cache {
+  uint8_t* latent;            /* page p: e4m3 [page_size, d_latent] at latent + p * latent_page_stride */
+  uint8_t* rope;              /* page p: e4m3 [page_size, d_rope] at rope + p * rope_page_stride, rotated */
+  float* scale;               /* f32 [n_pages], a power of two for each page           */
+  int64_t latent_page_stride; /* bytes, % 16 == 0, page_size * d_latent .. 2^39        */
+  int64_t rope_page_stride;   /* bytes, % 16 == 0, page_size * d_rope .. 2^39          */
+  int32_t n_pages;            /* pages of the pool, >= 1                               */
+  int32_t page_size;          /* tokens of a page                                      */
+  int32_t d_latent;
+  int32_t d_rope;
+} dsa_cache;
+
+/* A batch of sequences against the cache. Sequence b has seq_lens[b] rows, of
+ * which the last n_b = cu_seqlens[b+1] - cu_seqlens[b] are this step's: its
+ * token i (row cu_seqlens[b] + i of the call's token tensors) sits at position
+ * t = seq_lens[b] - n_b + i. Row t is in page page_table[b, t / page_size], at
+ * row t % page_size. All three arrays are read on the device, so a captured
+ * call replays with their new contents. Token rows before cu_seqlens[0] or
+ * from cu_seqlens[n_seq] on belong to no sequence: their outputs are left as
+ * they were. Page table entries that a call does not need are not read as
+ * pages and may hold anything.
+ * Checked on the device, for each sequence: 0 <= cu_seqlens[b] <=
+ * cu_seqlens[b+1] <= n_tok, n_b <= seq_lens[b] <= max_pages * page_size; a
+ * sequence that fails is skipped (its outputs are not written), a page outside
+ * 0..n_pages-1 is skipped (its rows are not written, or not seen), and either
+ * sets DSA_ERR_RANGE in the workspace status. Wrong cu_seqlens of one sequence
+ * may hide others. */
+typedef struct dsa_batch {
+  const int32_t* page_table; /* int32 [n_seq, max_pages]                               */
+  const int32_t* cu_seqlens; /* int32 [n_seq + 1], ascending                           */
+  const int32_t* seq_lens;   /* int32 [n_seq]                                          */
+  int32_t n_seq;             /* >= 0; 0 launches no kernel                             */
+  int32_t max_pages;         /* >= 1                                                   */
+  int32_t n_tok;             /* rows of the call's token tensors, >= 0                 */
+  int32_t reserved;          /* 0                                                      */
+} dsa_batch;
+
+/* Bytes of device workspace for any of the three calls below on a batch of at
+ * most this n_tok and n_seq with n_heads query heads (0 on bad arguments; only
+ * the sizes in the structs are read). Needs no initialisation. */
+size_t dsa_cache_workspace_size(const dsa_cache* cache, const dsa_batch* batch, int32_t n_heads);
+
+/* Which elements the rotation pairs: (2j, 2j+1), or (j, j + d_rope/2). */
+#define DSA_ROPE_INTERLEAVED 0
+#define DSA_ROPE_HALVES 1
+
+/* Appends the batch's new rows to the cache, rotated by their positions, and
+ * rotates the queries' rotary part on the way. For the token at position t
+ * and j < d_rope/2, with angle a = t * inv_freq[j] in float64:
+ *     (x, y) -> (x cos a - y sin a, y cos a + x sin a)
+ * on every pair (x, y) of the style. For each page that gets new rows, with
+ * `need` the smallest power of two s >= 2^-32 such that every |value| of the
+ * new rows (latent and rotated rope, float64) is at most 448 s:
+ *     s = need                 if the page's row 0 is among the new rows
+ *     s = max(scale[p], need)  otherwise; rows before the new ones are
+ *                              re-expressed when s grows: code = e4m3(code * scale[p] / s)
+ *     code = e4m3(value / s), scale[p] = s
+ * e4m3 rounds to nearest, ties to even. Rows behind the new ones keep their
+ * bytes. Calling it again with the same arguments changes nothing.
+ *   latent  bf16 [n_tok, d_latent], rows ld_latent elements apart
+ *   rope    bf16 [n_tok, d_rope], rows ld_rope elements apart (not rotated)
+ *   inv_freq f32 [d_rope / 2] (a rotation that is wanted for some pairs only
+ *           has 0 for the others)
+ *   q_rope  bf16 [n_tok, n_heads, d_rope] (not rotated), or NULL: token rows
+ *           ld_q_tok and heads ld_q_head elements apart
+ *   q       bf16 [n_tok, n_heads, d_latent + d_rope] or NULL with q_rope: its
+ *           last d_rope elements of each row receive the rotated q_rope (the
+ *           rest is not touched): the q of dsa_cache_attn
+ * The ld are multiples of 8, and their rows must not overlap in q.
+ * No page may receive rows of two sequences. Inputs may not alias outputs.
+ * Errors: DSA_ERR_NULL, _ALIGN (an ld too), _DIMS, _WORKSPACE, _DEVICE, _CUDA. */
+dsa_status dsa_cache_append(const dsa_cache* cache, const dsa_batch* batch,
+                            const uint16_t* latent, int64_t ld_latent, const uint16_t* rope,
+                            int64_t ld_rope, const float* inv_freq, int32_t rope_style,
+                            const uint16_t* q_rope, int64_t ld_q_tok, int64_t ld_q_head,
+                            uint16_t* q, int32_t n_heads, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/* Rows pos0 .. pos0 + n_rows - 1 of sequence `seq` as bf16 (exact):
+ *   latent  bf16 [n_rows, d_latent], rope bf16 [n_rows, d_rope] (outputs)
+ * i.e. the latent and rope that the contiguous calls of this header take.
+ * cu_seqlens and n_tok are not used. pos0 + n_rows <= seq_lens[seq] is checked
+ * on the device (DSA_ERR_RANGE; rows past it, and rows of a page outside the
+ * pool, are not written). n_rows == 0 launches no kernel.
+ * Errors: DSA_ERR_NULL, _ALIGN, _DIMS (a seq or range that cannot be),
+ * _WORKSPACE, _DEVICE, _CUDA. */
+dsa_status dsa_cache_gather(const dsa_cache* cache, const dsa_batch* batch, int32_t seq,
+                            int32_t pos0, int32_t n_rows, uint16_t* latent, uint16_t* rope,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* Attention of the batch's new tokens over the cache (their own rows
+ * included: append first). The token at position t sees, with window == 0,
+ * every row s <= t; with window >= 1 the rows t - window < s <= t and the
+ * first n_sink rows (s < n_sink, s <= t). For each head h:
+ *     z_s = softmax_scale * q[i,h,:] . row[s]         row = code * scale
+ *     out[i,h,:] = sum_s softmax(z)_s * row[s,:d_latent]
+ *     lse[i,h]   = log sum_s exp(z_s)
+ * bf16 q and out, float32 logits, softmax sums and accumulation. A token
+ * whose visible rows all lie in skipped pages gets out = 0 and lse = -inf.
+ *   q    bf16 [n_tok, n_heads, d_latent + d_rope], finite, rotated
+ *   out  bf16 [n_tok, n_heads, d_latent] (output)
+ *   lse  f32  [n_tok, n_heads] (output) or NULL
+ * Visible rows must be finite (append writes no other codes); bytes of rows
+ * that no token of the batch's sequence sees may be anything. The work of a
+ * long sequence is spread over SMs, so sums may be grouped differently for
+ * another batch or GPU; the same call gives the same bits.
+ * Errors: DSA_ERR_NULL, _ALIGN, _DIMS, _WORKSPACE, _DEVICE, _CUDA. */
+dsa_status dsa_cache_attn(const dsa_cache* cache, const dsa_batch* batch, const uint16_t* q,
+                          int32_t n_heads, float softmax_scale, int32_t window, int32_t n_sink,
+                          uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
 /* Multi-GPU prefill of one chunk: splits its queries into n_parts contiguous
  * ranges, one per rank, with nearly equal useful work. Row i (position t)
  * costs (t+1) * 2 * n_idx_heads * d_idx multiply-adds in the indexer and

@@ -52,6 +52,9 @@ DSA_FLAG_HOST_UNORDERED = 4
 DSA_FLAG_L2_SCORES = 8
 DSA_MAX_BLOCK_QUERIES = 2
 
+DSA_ROPE_INTERLEAVED = 0
+DSA_ROPE_HALVES = 1
+
 DSA_MAX_TOPK = 2048
 DSA_MAX_CTX = 131072
 
@@ -60,7 +63,8 @@ EXPORTED = ("dsa_workspace_size", "dsa_index_scores", "dsa_topk_select",
             "dsa_status_string", "dsa_prefill_layer_noalloc", "dsa_prefill_layer_host",
             "dsa_selftest_bounded_wait", "dsa_partition_queries", "dsa_sparse_attn_decode",
             "dsa_decode_layer", "dsa_sparse_attn_block", "dsa_quantize_fp8",
-            "dsa_index_scores_fp8", "dsa_selftest_mma_layout")
+            "dsa_index_scores_fp8", "dsa_selftest_mma_layout", "dsa_cache_workspace_size",
+            "dsa_cache_append", "dsa_cache_gather", "dsa_cache_attn")
 
 
 class dsa_dims(ctypes.Structure):
@@ -84,6 +88,32 @@ class dsa_device_tensors(ctypes.Structure):
                 ("q", "latent", "rope", "q_idx", "k_idx", "w_idx", "out", "lse", "idx")]
 
 
+class dsa_cache(ctypes.Structure):
+    _fields_ = [
+        ("latent", ctypes.c_void_p),
+        ("rope", ctypes.c_void_p),
+        ("scale", ctypes.c_void_p),
+        ("latent_page_stride", ctypes.c_int64),
+        ("rope_page_stride", ctypes.c_int64),
+        ("n_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("d_latent", ctypes.c_int32),
+        ("d_rope", ctypes.c_int32),
+    ]
+
+
+class dsa_batch(ctypes.Structure):
+    _fields_ = [
+        ("page_table", ctypes.c_void_p),
+        ("cu_seqlens", ctypes.c_void_p),
+        ("seq_lens", ctypes.c_void_p),
+        ("n_seq", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("n_tok", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
 class DsaError(RuntimeError):
     def __init__(self, status: int):
         super().__init__(f"dsa status {status}: {dsa_status_string(status)}")
@@ -92,6 +122,8 @@ class DsaError(RuntimeError):
 
 _P = ctypes.c_void_p
 _DP = ctypes.POINTER(dsa_dims)
+_CP = ctypes.POINTER(dsa_cache)
+_BP = ctypes.POINTER(dsa_batch)
 
 
 def library():
@@ -128,6 +160,14 @@ def library():
     lib.dsa_selftest_mma_layout.argtypes = [_P, ctypes.c_size_t, ctypes.POINTER(ctypes.c_int32),
                                             ctypes.POINTER(ctypes.c_float), _P]
     lib.dsa_partition_queries.argtypes = [_DP, ctypes.c_int32, ctypes.POINTER(ctypes.c_int32)]
+    i32, i64, size = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    lib.dsa_cache_workspace_size.argtypes = [_CP, _BP, i32]
+    lib.dsa_cache_workspace_size.restype = size
+    lib.dsa_cache_append.argtypes = [_CP, _BP, _P, i64, _P, i64, _P, i32, _P, i64, i64, _P, i32, _P,
+                                     size, _P]
+    lib.dsa_cache_gather.argtypes = [_CP, _BP, i32, i32, i32, _P, _P, _P, size, _P]
+    lib.dsa_cache_attn.argtypes = [_CP, _BP, _P, i32, ctypes.c_float, i32, i32, _P, _P, _P, size,
+                                   _P]
     lib.dsa_device_status.argtypes = [_P, _P]
     lib.dsa_status_string.argtypes = [ctypes.c_int32]
     lib.dsa_status_string.restype = ctypes.c_char_p
@@ -135,7 +175,8 @@ def library():
               "dsa_prefill_layer", "dsa_device_status", "dsa_prefill_layer_noalloc",
               "dsa_prefill_layer_host", "dsa_selftest_bounded_wait", "dsa_partition_queries",
               "dsa_sparse_attn_decode", "dsa_decode_layer", "dsa_sparse_attn_block",
-              "dsa_quantize_fp8", "dsa_index_scores_fp8", "dsa_selftest_mma_layout"):
+              "dsa_quantize_fp8", "dsa_index_scores_fp8", "dsa_selftest_mma_layout",
+              "dsa_cache_append", "dsa_cache_gather", "dsa_cache_attn"):
         getattr(lib, f).restype = ctypes.c_int32
     _lib = lib
     return lib
@@ -309,3 +350,85 @@ def dsa_partition_queries(dims, n_parts: int, starts=None):
     if starts is not None:
         starts[:] = out
     return st, out
+
+
+def make_cache(latent, rope, scale) -> dsa_cache:
+    """dsa_cache of three device tensors: latent and rope, one byte an element,
+    [n_pages, page_size, width] with dense pages (the stride between pages is
+    taken from the tensor), and scale, float32 [n_pages]. The struct keeps the
+    tensors alive."""
+    for name, x in (("latent", latent), ("rope", rope)):
+        if x.dim() != 3 or x.element_size() != 1 or (
+                x.numel() and (x.stride(2) != 1 or x.stride(1) != x.shape[2])):
+            raise ValueError(f"{name}: [n_pages, page_size, width] of one-byte elements with dense "
+                             "pages is wanted")
+    if latent.shape[:2] != rope.shape[:2] or tuple(scale.shape) != (latent.shape[0],) or \
+            str(scale.dtype) != "torch.float32" or not scale.is_contiguous():
+        raise ValueError("latent, rope and scale (float32 [n_pages]) do not belong together")
+    pages, size, dc = latent.shape
+    # a pool of one page may have any stride; the call checks the lower bound
+    c = dsa_cache(latent.data_ptr(), rope.data_ptr(), scale.data_ptr(),
+                  latent.stride(0) if pages > 1 else size * dc,
+                  rope.stride(0) if pages > 1 else size * rope.shape[2], pages, size, dc,
+                  rope.shape[2])
+    c.tensors = (latent, rope, scale)
+    return c
+
+
+def make_batch(page_table, cu_seqlens, seq_lens, n_tok: int) -> dsa_batch:
+    """dsa_batch of three int32 device tensors: page_table [n_seq, max_pages],
+    cu_seqlens [n_seq + 1] and seq_lens [n_seq], all dense; n_tok is the number
+    of rows of the calls' token tensors. The struct keeps the tensors alive."""
+    n_seq = seq_lens.shape[0]
+    for x in (page_table, cu_seqlens, seq_lens):
+        if str(x.dtype) != "torch.int32" or not x.is_contiguous():
+            raise ValueError("dense int32 tensors are wanted")
+    if page_table.dim() != 2 or page_table.shape[0] != n_seq or cu_seqlens.shape != (n_seq + 1,) or \
+            seq_lens.dim() != 1:
+        raise ValueError("page_table [n_seq, max_pages], cu_seqlens [n_seq + 1] and seq_lens "
+                         "[n_seq] do not belong together")
+    b = dsa_batch(page_table.data_ptr(), cu_seqlens.data_ptr(), seq_lens.data_ptr(), n_seq,
+                  page_table.shape[1], int(n_tok), 0)
+    b.tensors = (page_table, cu_seqlens, seq_lens)
+    return b
+
+
+def _ld(ld, x, dim, default):
+    """A stride in elements: the one given, else the tensor's, else the dense one."""
+    if ld is not None:
+        return int(ld)
+    if x is None or isinstance(x, int):
+        return default
+    if x.shape[-1] > 1 and x.stride(-1) != 1:
+        raise ValueError("rows have to be dense in their last dimension")
+    return x.stride(dim) if x.shape[dim] > 1 else default
+
+
+def dsa_cache_workspace_size(cache, batch, n_heads: int) -> int:
+    return int(library().dsa_cache_workspace_size(cache, batch, int(n_heads)))
+
+
+def dsa_cache_append(cache, batch, latent, rope, inv_freq, rope_style, q_rope, q, n_heads,
+                     workspace, workspace_bytes=None, stream=None, ld_latent=None, ld_rope=None,
+                     ld_q_tok=None, ld_q_head=None) -> int:
+    """Strides are taken from the tensors unless given (see include/dsa.h)."""
+    dr = cache.d_rope
+    return library().dsa_cache_append(
+        cache, batch, _p(latent), _ld(ld_latent, latent, 0, cache.d_latent), _p(rope),
+        _ld(ld_rope, rope, 0, dr), _p(inv_freq), int(rope_style), _p(q_rope),
+        _ld(ld_q_tok, q_rope, 0, n_heads * dr), _ld(ld_q_head, q_rope, 1, dr), _p(q), int(n_heads),
+        _p(workspace), _nbytes(workspace, workspace_bytes), _stream(stream))
+
+
+def dsa_cache_gather(cache, batch, seq, pos0, n_rows, latent, rope, workspace,
+                     workspace_bytes=None, stream=None) -> int:
+    return library().dsa_cache_gather(cache, batch, int(seq), int(pos0), int(n_rows), _p(latent),
+                                      _p(rope), _p(workspace), _nbytes(workspace, workspace_bytes),
+                                      _stream(stream))
+
+
+def dsa_cache_attn(cache, batch, q, n_heads, softmax_scale, window, n_sink, out, lse, workspace,
+                   workspace_bytes=None, stream=None) -> int:
+    return library().dsa_cache_attn(cache, batch, _p(q), int(n_heads), float(softmax_scale),
+                                    int(window), int(n_sink), _p(out), _p(lse), _p(workspace),
+                                    _nbytes(workspace, workspace_bytes), _stream(stream))
