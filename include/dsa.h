@@ -410,12 +410,11 @@ typedef struct dsa_cache {
  * from cu_seqlens[n_seq] on belong to no sequence: their outputs are left as
  * they were. Page table entries that a call does not need are not read as
  * pages and may hold anything.
- * Checked on the device, for each sequence: 0 <= cu_seqlens[b] <=
- * cu_seqlens[b+1] <= n_tok, n_b <= seq_lens[b] <= max_pages * page_size; a
- * sequence that fails is skipped (its outputs are not written), a page outside
+ * Checked on the device: a sequence without n_b <= seq_lens[b] <= max_pages *
+ * page_size is skipped (its outputs are not written), a page outside
  * 0..n_pages-1 is skipped (its rows are not written, or not seen), and either
- * sets DSA_ERR_RANGE in the workspace status. Wrong cu_seqlens of one sequence
- * may hide others. */
+ * sets DSA_ERR_RANGE in the workspace status, as do cu_seqlens that do not
+ * ascend within 0..n_tok: which sequences are skipped is not specified then. */
 typedef struct dsa_batch {
   const int32_t* page_table; /* int32 [n_seq, max_pages]                               */
   const int32_t* cu_seqlens; /* int32 [n_seq + 1], ascending                           */

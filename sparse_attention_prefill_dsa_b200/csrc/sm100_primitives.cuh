@@ -84,6 +84,15 @@ __device__ __forceinline__ void tma_load_2d(void* smem_dst, const CUtensorMap* m
       : "memory");
 }
 
+__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, int x, int y,
+                                            int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
@@ -157,9 +166,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn, b
 }
 
 // Instruction descriptor of kind::f8f6f4 with e4m3 A and B (format code 0),
-// float32 D, both operands K-major.
-__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
-  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+// float32 D, both operands K-major unless the *_mn flags are set.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, bool a_mn = false,
+                                                      bool b_mn = false) {
+  return (1u << 4) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
 // D[tmem] (+)= A[smem] * B[smem]^T, issued by one thread.
@@ -400,5 +411,10 @@ bool make_tmap_u8_2d(CUtensorMap* map, const void* base, uint64_t cols, uint64_t
                      uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle);
 bool make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
                        uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle);
+// Pages of bytes: [pages][rows][cols], pages `page_stride` bytes apart, with a
+// box of box_cols x rows of one page.
+bool make_tmap_u8_pages(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
+                        uint64_t pages, uint64_t page_stride, uint32_t box_cols,
+                        CUtensorMapSwizzle swizzle);
 
 }  // namespace dsa

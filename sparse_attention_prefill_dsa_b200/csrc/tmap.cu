@@ -57,4 +57,20 @@ bool make_tmap_u8_2d(CUtensorMap* map, const void* base, uint64_t cols, uint64_t
                       swizzle);
 }
 
+bool make_tmap_u8_pages(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
+                        uint64_t pages, uint64_t page_stride, uint32_t box_cols,
+                        CUtensorMapSwizzle swizzle) {
+  std::call_once(g_once, resolve);
+  if (!g_encode) return false;
+  const cuuint64_t dims[3] = {cols, rows, pages};
+  const cuuint64_t strides[2] = {cols, page_stride};
+  const cuuint32_t box[3] = {box_cols, static_cast<cuuint32_t>(rows), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims,
+                              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 }  // namespace dsa
