@@ -57,14 +57,14 @@ __device__ __forceinline__ bool page_ok(const dsa_cache& c, int page) {
 // floor((n - 1) / page_size) + 2 pages.
 __device__ void append_check(const AppendArgs& a) {
   unsigned int site = 0;
-  const int ps = a.cache.page_size;
+  const int ps = a.cache.page_size, shift = 31 - __clz(ps);
   for (int b = threadIdx.x; b < a.batch.n_seq; b += blockDim.x)
     if (!seq_range(a.batch, ps, b).ok) site = max(site, kCacheSiteSeq);
   const int64_t slots = a.batch.n_tok / ps + 2ll * a.batch.n_seq;
   for (int64_t s = threadIdx.x; s < slots; s += blockDim.x) {
-    const int b = seq_of_slot(a.batch, s, 1, ps, 2);
+    const int b = seq_of_slot(a.batch, s, 1, shift, 2);
     const SeqRange r = seq_range(a.batch, ps, b);
-    const int64_t j = s - slot_start(a.batch, b, 1, ps, 2);
+    const int64_t j = s - slot_start(a.batch, b, 1, shift, 2);
     if (r.n == 0 || j < 0) continue;
     const int64_t pg = (r.len - r.n) / ps + j;
     if (pg * ps < r.len && !page_ok(a.cache, page_of(a.batch, b, pg)))
@@ -130,9 +130,10 @@ template <int DC, int DR, int PS>
 __device__ void append_page(const AppendArgs& a, int64_t slot) {
   using C = AppendCfg<DC, DR, PS>;
   __shared__ int s_exp;
-  const int b = seq_of_slot(a.batch, slot, 1, PS, 2);
+  constexpr int kShift = PS == 16 ? 4 : PS == 32 ? 5 : PS == 64 ? 6 : 7;
+  const int b = seq_of_slot(a.batch, slot, 1, kShift, 2);
   const SeqRange r = seq_range(a.batch, PS, b);
-  const int64_t j = slot - slot_start(a.batch, b, 1, PS, 2);
+  const int64_t j = slot - slot_start(a.batch, b, 1, kShift, 2);
   if (r.n == 0 || j < 0) return;
   const int p0 = r.len - r.n;            // the sequence's first new position
   const int64_t pg = p0 / PS + j;        // this CTA's page of the sequence

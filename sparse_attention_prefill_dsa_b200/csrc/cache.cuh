@@ -43,22 +43,22 @@ __device__ __forceinline__ SeqRange seq_range(const dsa_batch& bt, int page_size
 
 // The sequences' slots of a grid that is sized without knowing cu_seqlens:
 // sequence b gets the slots [start(b), start(b + 1)), start(b) =
-// floor(cu_seqlens[b] * mul / div) + extra * b, which is ascending in b. A
-// sequence of n tokens then has at least floor(n * mul / div) + extra slots.
+// floor(cu_seqlens[b] * mul / 2^shift) + extra * b, which is ascending in b. A
+// sequence of n tokens then has at least floor(n * mul / 2^shift) + extra slots.
 // Returns the b whose slots hold `slot` (0 <= slot, n_seq >= 1). For
 // cu_seqlens that do not ascend it returns some b in range.
-__device__ __forceinline__ int64_t slot_start(const dsa_batch& bt, int b, int mul, int div,
+__device__ __forceinline__ int64_t slot_start(const dsa_batch& bt, int b, int mul, int shift,
                                               int extra) {
   const int64_t c = min(max(__ldg(bt.cu_seqlens + b), 0), bt.n_tok);
-  return c * mul / div + static_cast<int64_t>(extra) * b;
+  return ((c * mul) >> shift) + static_cast<int64_t>(extra) * b;
 }
 
-__device__ __forceinline__ int seq_of_slot(const dsa_batch& bt, int64_t slot, int mul, int div,
+__device__ __forceinline__ int seq_of_slot(const dsa_batch& bt, int64_t slot, int mul, int shift,
                                            int extra) {
   int lo = 0, hi = bt.n_seq - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (slot_start(bt, mid, mul, div, extra) <= slot) lo = mid;
+    if (slot_start(bt, mid, mul, shift, extra) <= slot) lo = mid;
     else hi = mid - 1;
   }
   return lo;

@@ -54,9 +54,7 @@ constexpr int kKeys = 128;
 constexpr int kChunkBytes = kKeys * 128;             // 128 dims of 128 keys
 constexpr int kRopeOff = 4 * kChunkBytes;            // the tile's rope chunk, 64-byte rows
 constexpr int kStageBytes = kRopeOff + kKeys * kDR;  // 72 KB
-constexpr int kThreads = 384;  // producer, MMA, two spare warps (the softmax warps start at a
-                               // multiple of four: a warp reads the TMEM lanes of its index mod 4)
-constexpr int kSoftmaxWarp0 = 4;
+constexpr int HR = 16;  // query rows of a softmax warpgroup
 
 // What a CTA leaves for the combine pass.
 struct CtaMeta {
@@ -96,22 +94,25 @@ __device__ __forceinline__ int64_t slots_of(const CacheAttnArgs& a) {
 
 template <int R>
 struct ItemWalk {
+  static constexpr int kShift = R == 32 ? 5 : 6;
   // Slot `slot` of the sequences' slots (R rows each), sequence b.
   int64_t slot, start, stop;
   int b;
   SeqRange r;
 
-  __device__ void load(const CacheAttnArgs& a) {
-    start = slot_start(a.batch, b, a.n_heads, R, 1);
-    stop = b + 1 < a.batch.n_seq ? slot_start(a.batch, b + 1, a.n_heads, R, 1) : INT64_MAX;
+  // (not inlined: the walk is off the critical paths, and the kernel's
+  // instructions have to stay within the instruction cache)
+  __device__ __noinline__ void load(const CacheAttnArgs& a) {
+    start = slot_start(a.batch, b, a.n_heads, kShift, 1);
+    stop = b + 1 < a.batch.n_seq ? slot_start(a.batch, b + 1, a.n_heads, kShift, 1) : INT64_MAX;
     r = seq_range(a.batch, a.cache.page_size, b);
   }
-  __device__ void seek(const CacheAttnArgs& a, int64_t s) {
+  __device__ __noinline__ void seek(const CacheAttnArgs& a, int64_t s) {
     slot = s;
-    b = seq_of_slot(a.batch, s, a.n_heads, R, 1);
+    b = seq_of_slot(a.batch, s, a.n_heads, kShift, 1);
     load(a);
   }
-  __device__ void next(const CacheAttnArgs& a) {
+  __device__ __noinline__ void next(const CacheAttnArgs& a) {
     ++slot;
     while (slot >= stop && b + 1 < a.batch.n_seq) {
       ++b;
@@ -119,7 +120,7 @@ struct ItemWalk {
     }
   }
   // Tiles of this slot's item, 0 when the sequence has no such rows.
-  __device__ int item(const CacheAttnArgs& a, Item& it) const {
+  __device__ __noinline__ int item(const CacheAttnArgs& a, Item& it) const {
     const int64_t rb = slot - start;
     const int64_t rows = static_cast<int64_t>(r.n) * a.n_heads;
     if (rb < 0 || rb * R >= rows) return 0;
@@ -139,10 +140,16 @@ struct ItemWalk {
   }
 };
 
-// A CTA's part of the tile list as segments: tiles [k0, k1) of one item after
-// the other. Every role walks its own copy.
+// Tiles [k0, k1) of an item, as the producer publishes them to the other
+// warps; more: the CTA has another segment after it.
+struct Segment {
+  Item it;
+  int k0, k1, more, pad;
+};
+
+// A CTA's part of the tile list as segments, one after the other.
 template <int R>
-struct Segments {
+struct SegmentWalk {
   ItemWalk<R> w;
   Item it;
   int k0, k1;
@@ -170,29 +177,22 @@ struct Segments {
   }
 };
 
-template <int R>
-struct Cfg {
-  static constexpr int HR = R / 2;                 // rows of a softmax warpgroup
-  static constexpr bool kSplitO = R == 32;         // hi and lo of P onto their own columns of O
-  static constexpr int kQChunk = 2 * R * 128;      // 128 dims of the hi and lo rows
-  static constexpr int kQBytes = 2 * R * (kDC + kDR);
-  static constexpr int kTmemS = 0, kTmemO = 4 * R;  // S^T [2 buffers][2R], O^T [4][64]
-  static constexpr int kOffQ = 0;
-  static constexpr int kOffStage = kQBytes;
-  static constexpr int kOffP = kOffStage + 2 * kStageBytes;
-  static constexpr int kOffM = kOffP + kKeys * 64;       // float [8 warps][32]
-  static constexpr int kOffRow = kOffM + 8 * 32 * 4;     // float rowfac[64], int row_t[64]
-  static constexpr int kOffBar = kOffRow + 2 * 64 * 4;
-  static constexpr int kNumBars = 10 + 10 + 2 + 2 + 5;
-  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr int kMiscBytes = 160;
-  static constexpr int kSmemBytes = kOffMisc + kMiscBytes + 1024;
-  static constexpr uint32_t kIdescQK = idesc_e4m3_f32(128, 2 * R);
-  static constexpr uint32_t kIdescPV = idesc_e4m3_f32(128, 64, true, true);
-  static_assert(kOffStage % 1024 == 0 && kOffP % 1024 == 0, "operand alignment");
-  static_assert(kSmemBytes <= 232448, "shared memory");
-  static_assert(kTmemO + 256 <= 512, "tensor memory");
+// Published segments. The producer publishes a segment two tiles before it
+// loads its first; a tile's place is loaded again once its PV is done, which
+// every warp has taken part in. So the warp that is furthest behind is at most
+// five tiles, and segments, behind.
+constexpr int kSegSlots = 8;
+static_assert(sizeof(Segment) <= 64, "segment slot");
+
+// What the producer tells the softmax of a tile, in a ring of four, a tile
+// before it loads it.
+struct TileInfo {
+  int exp[8];  // the scale exponents of its pages, kNoPage where nothing was loaded
+  int t0;      // first key
+  int masked;  // some row does not see some key
+  int pad[2];
 };
+static_assert(sizeof(TileInfo) == 48, "tile info");
 
 // Shared words after the barriers.
 struct Misc {
@@ -200,20 +200,94 @@ struct Misc {
   uint32_t tmem;
   int abort_flag;
   long long slot, n_tiles, total;
-  long long scan[12];
   int k0;
 };
-static_assert(sizeof(Misc) <= 160, "misc");
+static_assert(sizeof(Misc) <= 48, "misc");
 
-enum Bars { kFull = 0, kEmpty = 10, kSFull = 20, kSFree = 22, kPFull = 24, kPvDone, kQFull, kOFree, kDrain };
-enum Sites { kSiteEmpty = 40, kSiteFull, kSiteSFull, kSiteSFree, kSiteP, kSitePv, kSiteQ, kSiteO };
+// mbarriers: what TMA and the tensor cores arrive on, and rare events.
+enum Bars {
+  kFull = 0,              // [2 stages][5 chunks] a tile's chunk has landed
+  kEmpty = 10,            // [2][5] the PV is done with it
+  kSFull = 20,            // [2] QK^T of a tile is done
+  kPvDone = 22,           // PV of a tile is done
+  kQFull,                 // the segment's Q is written
+  kOFree,                 // the segment's O has been read
+  kSeg,                   // [kSegSlots] a segment is published
+  kInfo = kSeg + kSegSlots,  // [4] a tile's info is in place
+  kDrain = kInfo + 4,
+  kBarCount
+};
 
+// Hardware barriers. The MMAs read their operands from shared memory at its
+// full 128 bytes a clock, and whatever else reads it then waits for a gap
+// between two of them (a dependent load takes 114 clocks instead of 40, and
+// warps that poll an mbarrier wait for each other). So per tile one relay warp
+// polls for all softmax warps, and the rest of the exchange between them and
+// the MMA warp is on these, which take no shared memory.
+enum HwBars {
+  kVote = 1,    // [groups] within a softmax warpgroup
+  kAll = 5,     // all softmax warps
+  kSReady = 6,   // [2] relay -> softmax: S of a tile, and the info of the next. Two of
+                 // them, by the tile's parity: QK^T of two tiles can be done before
+                 // the softmax takes note of the first
+  kPvReady = 8,  // relay, softmax: PV of a tile is done
+  kSFree = 9,    // [2] softmax -> MMA: S has been read
+  kPReady = 11   // softmax -> MMA: P is written
+};
+
+template <int R>
+struct Cfg {
+  static constexpr int kGroups = R / HR;           // softmax warpgroups: warps 0 .. 4 kGroups - 1
+  static constexpr int kWarps = 4 * kGroups;       // (a warp reads the TMEM lanes of its index mod 4)
+  static constexpr int kThreads = 32 * (kWarps + 3);  // + producer, MMA, relay
+  static constexpr int kSync = 32 * (kWarps + 1);     // the softmax warps and one other
+  static constexpr bool kSplitO = R == 32;         // hi and lo of P onto their own columns of O
+  static constexpr int kQChunk = 2 * R * 128;      // 128 dims of the hi and lo rows
+  static constexpr int kQBytes = 2 * R * (kDC + kDR);
+  static constexpr int kTmemS = 0, kTmemO = 4 * R;  // S^T [2 buffers][2R], O^T [4][64]
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffStage = kQBytes;
+  static constexpr int kOffP = kOffStage + 2 * kStageBytes;
+  static constexpr int kOffM = kOffP + kKeys * 64;       // float [warps][HR]
+  static constexpr int kOffRow = kOffM + 16 * HR * 4;    // float rowfac[64], uint8 row_dt[64]
+  static constexpr int kOffSeg = kOffRow + 64 * 5;       // Segment [kSegSlots]
+  static constexpr int kOffTile = kOffSeg + kSegSlots * 64;  // TileInfo [4]
+  static constexpr int kOffBar = kOffTile + 4 * 48;
+  static constexpr int kNumBars = kBarCount;
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  static constexpr int kMiscBytes = 48;
+  static constexpr int kSmemBytes = kOffMisc + kMiscBytes;
+  static constexpr uint32_t kIdescQK = idesc_e4m3_f32(128, 2 * R);
+  static constexpr uint32_t kIdescPV = idesc_e4m3_f32(128, 64, true, true);
+  static_assert(kOffStage % 1024 == 0 && kOffP % 1024 == 0, "operand alignment");
+  static_assert(kSmemBytes <= 232448, "shared memory");
+  static_assert(kTmemO + 256 <= 512, "tensor memory");
+};
+
+enum Sites { kSiteEmpty = 40, kSiteFull, kSiteSFull, kSitePv, kSiteQ, kSiteO, kSiteSeg, kSiteInfo };
+
+constexpr int kNoPage = 1 << 20;
+
+// The kernel's shared memory: a symbol, so that operand addresses are
+// constants (uniform registers of the MMA warp). Swizzled operands need a
+// 1024-byte boundary, checked when the kernel starts.
+extern __shared__ __align__(1024) unsigned char cache_attn_smem[];
+
+// Hardware barriers by number. The warp has to be converged there; waits and
+// single-lane blocks before them may leave it split.
 __device__ __forceinline__ void named_sync(int id, int threads) {
+  __syncwarp();
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+__device__ __forceinline__ void named_arrive(int id, int threads) {
+  __syncwarp();
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 __device__ __forceinline__ bool named_or(int id, int threads, bool p) {
   uint32_t r;
+  __syncwarp();
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
@@ -231,16 +305,13 @@ __device__ __forceinline__ float warp_max(float x) {
   return y;
 }
 
-// Sum of v[e] over the 32 lanes for every e; lane l gets that of e = l % NV.
-template <int NV>
-__device__ __forceinline__ float warp_transpose_sum(float (&v)[NV]) {
+// Sum of v[e] over the 32 lanes for every e; lane l gets that of e = l % 16.
+__device__ __forceinline__ float warp_transpose_sum(float (&v)[16]) {
   const int lane = threadIdx.x & 31;
-  if constexpr (NV == 16) {
 #pragma unroll
-    for (int e = 0; e < NV; ++e) v[e] += __shfl_xor_sync(0xffffffffu, v[e], 16);
-  }
+  for (int e = 0; e < 16; ++e) v[e] += __shfl_xor_sync(0xffffffffu, v[e], 16);
 #pragma unroll
-  for (int s = NV / 2; s >= 1; s >>= 1) {
+  for (int s = 8; s >= 1; s >>= 1) {
     const bool upper = (lane & s) != 0;
 #pragma unroll
     for (int e = 0; e < s; ++e) {
@@ -252,29 +323,41 @@ __device__ __forceinline__ float warp_transpose_sum(float (&v)[NV]) {
   return v[0];
 }
 
-template <int NC>
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[NC]) {
-  if constexpr (NC == 32) tmem_ld_32x32b_x32(taddr, r);
-  else tmem_ld_32x32b_x16(taddr, r);
-}
-
-template <int NC>
-__device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t (&r)[NC]) {
-  if constexpr (NC == 32) tmem_st_32x32b_x32(taddr, r);
-  else tmem_st_32x32b_x16(taddr, r);
-}
-
 // ------------------------------------------------------------------ schedule
 
-// Counts the tiles of all items and finds this CTA's part. All threads.
+// CTA c's part of `total` tiles on `grid` CTAs starts at this tile (CTAs past
+// the number of tiles have none).
+__device__ __noinline__ long long part_begin(long long total, int grid, int c) {
+  const unsigned long long g = min(static_cast<long long>(grid), total);
+  if (static_cast<unsigned long long>(c) >= g) return total;
+  return static_cast<long long>(static_cast<unsigned long long>(total) * c / g);
+}
+
+// The CTA up to `last` whose part of the list holds tile `at`.
+__device__ __noinline__ int cta_of_tile(long long at, long long total, int grid, int last) {
+  int lo = 0;
+  while (lo < last) {
+    const int mid = (lo + last + 1) >> 1;
+    if (part_begin(total, grid, mid) <= at) lo = mid;
+    else last = mid - 1;
+  }
+  return lo;
+}
+
+// Counts the tiles of all items and finds this CTA's part. All threads;
+// `scan` is scratch for a long long of each warp.
 template <int R>
-__device__ void schedule(const CacheAttnArgs& a, Misc* ms) {
+__device__ void schedule(const CacheAttnArgs& a, Misc* ms, long long* scan) {
+  constexpr int kThreads = Cfg<R>::kThreads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // the slots need cu_seqlens that ascend; if they do not, there is no work
   int bad = 0;
   for (int b = tid; b < a.batch.n_seq; b += kThreads) {
-    const int c0 = __ldg(a.batch.cu_seqlens + b), c1 = __ldg(a.batch.cu_seqlens + b + 1);
-    bad |= c0 < 0 || c1 < c0 || c1 > a.batch.n_tok;
+    const SeqRange r = seq_range(a.batch, a.cache.page_size, b);
+    const int c1 = __ldg(a.batch.cu_seqlens + b + 1);
+    bad |= r.tok0 < 0 || c1 < r.tok0 || c1 > a.batch.n_tok;
+    if (!r.ok && blockIdx.x == 0)
+      report(reinterpret_cast<WsHeader*>(&ms->status), kDevRange, kCacheSiteSeq);
   }
   const int64_t slots = __syncthreads_or(bad) ? 0 : slots_of<R>(a);
   const int64_t per = (slots + kThreads - 1) / kThreads;
@@ -295,19 +378,15 @@ __device__ void schedule(const CacheAttnArgs& a, Misc* ms) {
     const long long v = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += v;
   }
-  if (lane == 31) ms->scan[warp] = inc;
+  if (lane == 31) scan[warp] = inc;
   __syncthreads();
   long long before = 0, total = 0;
   for (int i = 0; i < kThreads / 32; ++i) {
-    if (i < warp) before += ms->scan[i];
-    total += ms->scan[i];
+    if (i < warp) before += scan[i];
+    total += scan[i];
   }
-  const long long g = min(static_cast<long long>(gridDim.x), total);  // CTAs with work
-  long long begin = 0, end = 0;
-  if (static_cast<long long>(blockIdx.x) < g) {
-    begin = total * blockIdx.x / g;
-    end = total * (blockIdx.x + 1) / g;
-  }
+  const long long begin = part_begin(total, gridDim.x, blockIdx.x);
+  const long long end = part_begin(total, gridDim.x, blockIdx.x + 1);
   const long long lo = before + inc - sum;
   if (begin < end && lo <= begin && begin < lo + sum) {  // one thread
     long long at = lo;
@@ -327,16 +406,13 @@ __device__ void schedule(const CacheAttnArgs& a, Misc* ms) {
   __syncthreads();
 }
 
-// The CTA whose part of the list holds tile `at`.
-__device__ __forceinline__ int cta_of_tile(long long at, long long total, int grid) {
-  const long long g = min(static_cast<long long>(grid), total);
-  long long c = at * g / total;
-  while (c + 1 < g && total * (c + 1) / g <= at) ++c;
-  while (c > 0 && total * c / g > at) --c;
-  return static_cast<int>(c);
-}
-
 // ---------------------------------------------------------------- q operand
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 
 // The exponent e of the smallest 2^e with |x| <= 448 * 2^e.
 __device__ __forceinline__ int q_exp(float amax) {
@@ -349,106 +425,134 @@ __device__ __forceinline__ float2 bf16x2(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
-// Eight bf16 as e4m3 hi and lo codes: x * inv = hi + lo / 16.
-__device__ __forceinline__ void split_q(const uint4& v, float inv, uint2& hi, uint2& lo) {
+// Eight bf16 as e4m3 hi and lo codes: x * inv = hi + lo / 16. The steps in
+// between are in float16: |x * inv| <= 448, and its 11 bits hold a bf16's 8.
+__device__ __forceinline__ void split_q(const uint4& v, float inv, uint32_t (&hi)[2],
+                                        uint32_t (&lo)[2]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t h[4], l[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    float2 x = bf16x2(w[e]);
-    x.x *= inv;
-    x.y *= inv;
-    h[e] = f32_to_e4m3x2(x.x, x.y);
-    const float2 y = e4m3x2_to_f32(h[e]);
-    l[e] = f32_to_e4m3x2((x.x - y.x) * 16.f, (x.y - y.y) * 16.f);
+    const float2 x = bf16x2(w[e]);
+    const __half2 f = __floats2half2_rn(x.x * inv, x.y * inv);
+    h[e] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(f), __NV_SATFINITE, __NV_E4M3);
+    const __half2 b = __half2(
+        __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(h[e]), __NV_E4M3));
+    const __half2 r = __hmul2(__hsub2(f, b), __float2half2_rn(16.f));
+    l[e] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(r), __NV_SATFINITE, __NV_E4M3);
   }
-  hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
-  lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+  hi[0] = h[0] | h[1] << 16;
+  hi[1] = h[2] | h[3] << 16;
+  lo[0] = l[0] | l[1] << 16;
+  lo[1] = l[2] | l[3] << 16;
 }
 
-// Byte offset of group g (8 codes) of operand row n within the Q buffer.
+// Byte offset of 16-byte unit u (16 codes) of operand row n within the Q buffer.
 template <int R>
-__device__ __forceinline__ uint32_t q_off(int n, int g) {
-  if (g < kDC / 8) {
-    const int c = g >> 4, u = (g & 15) >> 1;  // chunk, 16-byte unit
-    return c * Cfg<R>::kQChunk + n * 128 + ((u ^ (n & 7)) << 4) + (g & 1) * 8;
-  }
-  const int u = (g - kDC / 8) >> 1;
-  return 4 * Cfg<R>::kQChunk + n * 64 + ((u ^ ((n >> 1) & 3)) << 4) + (g & 1) * 8;
+__device__ __forceinline__ uint32_t q_off(int n, int u) {
+  return u < kDC / 16 ? (u >> 3) * Cfg<R>::kQChunk + n * 128 + (((u & 7) ^ (n & 7)) << 4)
+                      : 4 * Cfg<R>::kQChunk + n * 64 + (((u & 3) ^ ((n >> 1) & 3)) << 4);
 }
 
 // The item's rows as operand rows (hi at r, lo at R + r), their factors and
-// positions. The eight softmax warps, a row at a time each.
+// positions (less t_lo). Each softmax warp takes four rows: 144 units of 16
+// elements, five for a lane.
 template <int R>
 __device__ void convert_q(const CacheAttnArgs& a, const Item& it, unsigned char* sq, float* rowfac,
-                          int* row_t) {
-  const int warp = (threadIdx.x >> 5) - kSoftmaxWarp0, lane = threadIdx.x & 31;
-  constexpr int kGroups = (kDC + kDR) / 8;  // 72
-  constexpr int kAtOnce = 4;
+                          uint8_t* row_dt) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kUnits = (kDC + kDR) / 16;  // 36 of a row
+  constexpr int kRows = 4, kRounds = (kRows * kUnits + 31) / 32;
+  static_assert(R == kRows * Cfg<R>::kWarps, "rows of a warp");
+  const uint4* src = reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(it.row) * (kDC + kDR));
+  const int r0 = warp * kRows, n_units = (min(it.n_rows, r0 + kRows) - r0) * kUnits;
+  src += r0 * kUnits * 2;
+  uint4 v[kRounds][2];
 #pragma unroll
-  for (int j0 = 0; j0 < R / 8; j0 += kAtOnce) {
-    uint4 v[kAtOnce][3];
-#pragma unroll
-    for (int j = 0; j < kAtOnce; ++j) {
-      const int r = warp + 8 * (j0 + j);
-      const uint4* src = reinterpret_cast<const uint4*>(
-          a.q + (static_cast<int64_t>(it.row) + r) * (kDC + kDR));
-#pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        v[j][i] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < it.n_rows && lane + 32 * i < kGroups) v[j][i] = __ldg(src + lane + 32 * i);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < kAtOnce; ++j) {
-      const int r = warp + 8 * (j0 + j);
-      float mx = 0.f;
-#pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        const uint32_t w[4] = {v[j][i].x, v[j][i].y, v[j][i].z, v[j][i].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 x = bf16x2(w[e]);
-          mx = fmaxf(mx, fmaxf(fabsf(x.x), fabsf(x.y)));
-        }
-      }
-      const int e = q_exp(warp_max(mx));
-      const float inv = pow2f(-e);
-#pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        const int g = lane + 32 * i;
-        if (g < kGroups) {
-          uint2 hi, lo;
-          split_q(v[j][i], inv, hi, lo);
-          *reinterpret_cast<uint2*>(sq + q_off<R>(r, g)) = hi;
-          *reinterpret_cast<uint2*>(sq + q_off<R>(R + r, g)) = lo;
-        }
-      }
-      if (lane == 0) {
-        rowfac[r] = pow2f(e) * a.scale_log2;
-        row_t[r] = it.first + (it.i0 + min(r, it.n_rows - 1)) / a.n_heads;
-      }
+  for (int i = 0; i < kRounds; ++i) {
+    const int x = lane + 32 * i;
+    v[i][0] = v[i][1] = make_uint4(0u, 0u, 0u, 0u);
+    if (x < n_units) {
+      v[i][0] = __ldg(src + 2 * x);
+      v[i][1] = __ldg(src + 2 * x + 1);
     }
   }
+  // the rows' largest |x|: bf16 magnitudes order as integers
+  uint32_t mx[kRows] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    const uint32_t w[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w,
+                           v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
+    uint32_t m = 0u;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max_u16x2(m, w[e] & 0x7FFF7FFFu);
+    m = max(m & 0xFFFFu, m >> 16);
+    const int j = (lane + 32 * i) / kUnits;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+      if (32 * i < (r + 1) * kUnits && 32 * i + 31 >= r * kUnits) mx[r] = max(mx[r], j == r ? m : 0u);
+  }
+  int e_row[kRows];
+#pragma unroll
+  for (int r = 0; r < kRows; ++r)
+    e_row[r] = q_exp(__uint_as_float(__reduce_max_sync(0xffffffffu, mx[r]) << 16));
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    const int x = lane + 32 * i, j = x / kUnits, u = x - j * kUnits;
+    if (j >= kRows) continue;
+    int e = e_row[0];
+#pragma unroll
+    for (int r = 1; r < kRows; ++r) e = j == r ? e_row[r] : e;
+    const float inv = pow2f(-e);
+    uint32_t h0[2], l0[2], h1[2], l1[2];
+    split_q(v[i][0], inv, h0, l0);
+    split_q(v[i][1], inv, h1, l1);
+    *reinterpret_cast<uint4*>(sq + q_off<R>(r0 + j, u)) = make_uint4(h0[0], h0[1], h1[0], h1[1]);
+    *reinterpret_cast<uint4*>(sq + q_off<R>(R + r0 + j, u)) = make_uint4(l0[0], l0[1], l1[0], l1[1]);
+  }
+#pragma unroll
+  for (int r = 0; r < kRows; ++r)
+    if (lane == r) {
+      rowfac[r0 + r] = pow2f(e_row[r]) * a.scale_log2;
+      row_dt[r0 + r] = static_cast<uint8_t>(
+          it.first + (it.i0 + min(r0 + r, it.n_rows - 1)) / a.n_heads - it.t_lo);
+    }
 }
 
 // -------------------------------------------------------------------- kernel
 
+// The polling loop of a wait, once for all waits.
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, Misc* ms, unsigned site) {
+  return mbar_wait(bar, parity, &ms->abort_flag, reinterpret_cast<WsHeader*>(&ms->status), site);
+}
+
 template <int R>
 struct Ctx {
   const CacheAttnParams& p;
-  unsigned char* s;
-  uint64_t* bar;
-  Misc* ms;
-  uint32_t tmem;
-  __device__ bool wait(int b, uint32_t parity, unsigned site) const {
-    return mbar_wait(bar + b, parity, &ms->abort_flag, reinterpret_cast<WsHeader*>(&ms->status),
-                     site);
+  __device__ __forceinline__ unsigned char* s() const { return cache_attn_smem; }
+  __device__ __forceinline__ uint64_t* bar(int b) const {
+    return reinterpret_cast<uint64_t*>(cache_attn_smem + Cfg<R>::kOffBar) + b;
+  }
+  __device__ __forceinline__ Misc* ms() const {
+    return reinterpret_cast<Misc*>(cache_attn_smem + Cfg<R>::kOffMisc);
+  }
+  __device__ __forceinline__ Segment* segment(int seg) const {
+    return reinterpret_cast<Segment*>(cache_attn_smem + Cfg<R>::kOffSeg) + seg % kSegSlots;
+  }
+  __device__ __forceinline__ TileInfo* info(int i) const {
+    return reinterpret_cast<TileInfo*>(cache_attn_smem + Cfg<R>::kOffTile) + (i & 3);
+  }
+  __device__ __forceinline__ bool wait(int b, uint32_t parity, unsigned site) const {
+    return mbar_try_wait(bar(b), parity) || wait_on(bar(b), parity, ms(), site);
+  }
+  __device__ __forceinline__ bool wait_segment(int seg) const {
+    return wait(kSeg + seg % kSegSlots, (seg / kSegSlots) & 1, kSiteSeg);
   }
   __device__ void error(unsigned site) const {
-    report(reinterpret_cast<WsHeader*>(&ms->status), kDevRange, site);
+    report(reinterpret_cast<WsHeader*>(&ms()->status), kDevRange, site);
   }
 };
+static_assert(sizeof(Segment) == 64, "segments are an array of slots");
 
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
   const long long t0 = clock64();
@@ -456,69 +560,145 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
     if (clock64() - t0 > kWaitLimitCycles) break;
 }
 
+// The order of a CTA's matrix products, as the MMA warp issues them and the
+// relay warp sees them done: QK^T runs one tile ahead of PV, but a segment's
+// first QK^T comes after the last PV of the segment before (whose epilogue
+// then overlaps it).
+template <int R>
+struct Order {
+  int q = 0, v = 0;      // next tiles of QK^T and PV
+  int seg = 0, left = 0; // segment of tile q, its tiles from q on (0: not looked at yet)
+  int n;
+  __device__ __forceinline__ bool pv_next() const { return q - v == 2 || (v < q && (q == n || left == 0)); }
+  // Before QK^T of tile q: looks up its segment if it begins one.
+  __device__ __forceinline__ bool begin_q(const Ctx<R>& x, bool& ok) {
+    if (left > 0) return false;
+    ok = ok && x.wait_segment(seg);
+    ok = __all_sync(0xffffffffu, ok);
+    left = ok ? x.segment(seg)->k1 - x.segment(seg)->k0 : n - q;
+    return true;
+  }
+  __device__ __forceinline__ void end_q() {
+    ++q;
+    if (--left == 0) ++seg;
+  }
+};
+
 // Producer warp: lane l < 128 / page_size loads the tile's l-th page.
 template <int R>
 __device__ void producer(const Ctx<R>& x, const CUtensorMap* ml, const CUtensorMap* mr) {
   const CacheAttnArgs& a = x.p.a;
   const int lane = threadIdx.x & 31, ps = a.cache.page_size, npt = kKeys / ps;
-  Segments<R> sg;
-  sg.begin(a, x.ms->slot, x.ms->k0, x.ms->n_tiles);
-  int i = 0, c_failed = 0;
-  bool ok = true;
-  int page_next = -1;
-  // this lane's page of tile k, or -1 when no row of the item sees any of it
-  auto page_of = [&](int k) {
-    if (lane >= npt) return -1;
-    const int s0 = sg.it.tile(k) * kKeys + lane * ps, s1 = s0 + ps - 1;
-    const bool any = s0 <= sg.it.t_hi && (s1 >= sg.it.win_lo || s0 < sg.it.sink_hi);
-    if (!any) return -1;
-    const int pg = __ldg(a.batch.page_table + static_cast<int64_t>(sg.it.b) * a.batch.max_pages +
-                         s0 / ps);
-    if (pg >= 0 && pg < a.cache.n_pages) return pg;
-    x.error(kCacheSitePage);
-    return -1;
+  const int n = static_cast<int>(x.ms()->n_tiles);
+  SegmentWalk<R> sg;
+  sg.begin(a, x.ms()->slot, x.ms()->k0, x.ms()->n_tiles);
+  int seg = 0;
+  auto publish = [&] {
+    if (lane == 0) {
+      Segment* out = x.segment(seg);
+      out->it = sg.it;
+      out->k0 = sg.k0;
+      out->k1 = sg.k1;
+      out->more = sg.left > 0;
+      mbar_arrive(x.bar(kSeg + seg % kSegSlots));
+    }
+    ++seg;
   };
-  do {
-    page_next = page_of(sg.k0);
-    for (int k = sg.k0; k < sg.k1 && ok; ++k, ++i) {
-      const int page = page_next;
-      if (k + 1 < sg.k1) page_next = page_of(k + 1);
-      const int n = __popc(__ballot_sync(0xffffffffu, page >= 0));
-      const int st = i & 1;
-      unsigned char* dst = x.s + Cfg<R>::kOffStage + st * kStageBytes;
-      for (int c = 0; c < 5; ++c) {
-        if (i >= 2) ok = x.wait(kEmpty + 5 * st + c, ((i >> 1) - 1) & 1, kSiteEmpty);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) {
-          c_failed = c;
-          break;
-        }
-        uint64_t* full = x.bar + kFull + 5 * st + c;
-        const int row_bytes = c < 4 ? 128 : kDR;
-        if (lane == 0) mbar_arrive_expect_tx(full, n * ps * row_bytes);
-        __syncwarp();
-        if (page >= 0) {
-          if (c < 4) tma_load_3d(dst + c * kChunkBytes + lane * ps * 128, ml, c * 128, 0, page, full);
-          else tma_load_3d(dst + kRopeOff + lane * ps * kDR, mr, 0, 0, page, full);
+  publish();
+  if (lane == 0) {
+    // an item that began in another CTA and ends here: this CTA's entry tells
+    // the combine pass of it
+    CtaMeta& me = x.p.meta[blockIdx.x];
+    me.n_rows = 0;
+    if (sg.k0 > 0 && sg.k1 == sg.it.nt) {
+      me.row = sg.it.row;
+      me.n_rows = sg.it.n_rows;
+      me.first = cta_of_tile(part_begin(x.ms()->total, gridDim.x, blockIdx.x) - sg.k0,
+                             x.ms()->total, gridDim.x, blockIdx.x);
+    }
+  }
+  // The next tile to plan is tile k of the segment. Its plan: this lane's page
+  // (-1 when no row of the item sees any of it), its first key, whether all
+  // rows see all of it.
+  int k = sg.k0, page = -1, t0 = 0;
+  bool whole = false;
+  auto plan = [&] {
+    t0 = sg.it.tile(k) * kKeys;
+    whole = t0 + kKeys - 1 <= sg.it.t_lo &&
+            (a.window == 0 || t0 > sg.it.t_hi - a.window || t0 + kKeys <= a.n_sink);
+    page = -1;
+    if (lane < npt) {
+      const int s0 = t0 + lane * ps, s1 = s0 + ps - 1;
+      if (s0 <= sg.it.t_hi && (s1 >= sg.it.win_lo || s0 < sg.it.sink_hi)) {
+        page = __ldg(a.batch.page_table + static_cast<int64_t>(sg.it.b) * a.batch.max_pages + s0 / ps);
+        if (page < 0 || page >= a.cache.n_pages) {
+          x.error(kCacheSitePage);
+          page = -1;
         }
       }
     }
-  } while (ok && sg.next(a));
+    if (++k == sg.k1 && sg.next(a)) {
+      k = sg.k0;
+      publish();
+    }
+  };
+  auto tell = [&](int i, int pg, int first, bool all) {
+    const bool has = lane >= npt || pg >= 0;
+    const int e = lane < npt && pg >= 0 ? scale_exp(__ldg(a.cache.scale + pg)) : kNoPage;
+    const bool full = all && __all_sync(0xffffffffu, has);
+    TileInfo* out = x.info(i);
+    if (lane < npt) out->exp[lane] = e;
+    if (lane == 0) {
+      out->t0 = first;
+      out->masked = !full;
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(x.bar(kInfo + (i & 3)));
+  };
+  plan();
+  bool ok = true;
+  int c_failed = 0, i = 0;
+  for (; i < n && ok; ++i) {
+    const int pg = page, first = t0;
+    const bool all = whole;
+    if (i + 1 < n) plan();
+    const int bytes = __popc(__ballot_sync(0xffffffffu, pg >= 0)) * ps;
+    const int st = i & 1;
+    unsigned char* dst = x.s() + Cfg<R>::kOffStage + st * kStageBytes;
+#pragma unroll 1
+    for (int c = 0; c < 5; ++c) {
+      if (i >= 2) ok = x.wait(kEmpty + 5 * st + c, ((i >> 1) - 1) & 1, kSiteEmpty);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) {
+        c_failed = c;
+        break;
+      }
+      uint64_t* full = x.bar(kFull + 5 * st + c);
+      if (lane == 0) mbar_arrive_expect_tx(full, bytes * (c < 4 ? 128 : kDR));
+      __syncwarp();
+      if (pg >= 0) {
+        if (c < 4) tma_load_3d(dst + c * kChunkBytes + lane * ps * 128, ml, c * 128, 0, pg, full);
+        else tma_load_3d(dst + kRopeOff + lane * ps * kDR, mr, 0, 0, pg, full);
+      }
+    }
+    if (i == 0) tell(0, pg, first, all);
+    if (i + 1 < n) tell(i + 1, page, t0, whole);
+  }
   if (!ok && lane == 0) {
     // Let the copies in flight land before the block ends: tile i - 1 was
     // begun up to chunk c_failed, the one before it in full.
     for (int c = 0; c < 5; ++c)
       for (int j = max(i - 3, 0); j < i; ++j)
-        if (j < i - 1 || c < c_failed) drain_wait(x.bar + kFull + 5 * (j & 1) + c, (j >> 1) & 1);
+        if (j < i - 1 || c < c_failed) drain_wait(x.bar(kFull + 5 * (j & 1) + c), (j >> 1) & 1);
   }
 }
 
-// MMA warp (warp-collective issue).
+// MMA warp: one thread issues. After a timeout it goes on through the
+// hardware barriers without issuing.
 template <int R>
 __device__ void mma_issuer(const Ctx<R>& x) {
   using C = Cfg<R>;
-  const CacheAttnArgs& a = x.p.a;
-  const uint32_t sb = smem_u32(x.s);
+  const uint32_t sb = smem_u32(cache_attn_smem);
   const uint64_t dq = smem_desc(sb + C::kOffQ, 16, 1024, 2);
   const uint64_t dqr = smem_desc(sb + C::kOffQ + 4 * C::kQChunk, 16, 512, 4);
   const uint64_t dk = smem_desc(sb + C::kOffStage, 16, 1024, 2);
@@ -526,193 +706,347 @@ __device__ void mma_issuer(const Ctx<R>& x) {
   const uint64_t dv = smem_desc(sb + C::kOffStage, 16384, 1024, 2);
   const uint64_t dp = smem_desc(sb + C::kOffP, 512, 512, 4);
   const uint64_t dph = smem_desc(sb + C::kOffStage + kRopeOff, 512, 512, 4);
-  Segments<R> sg;
-  sg.begin(a, x.ms->slot, x.ms->k0, x.ms->n_tiles);
-  int i = 0, seg = 0;
+  Order<R> o;
+  o.n = __shfl_sync(0xffffffffu, static_cast<int>(x.ms()->n_tiles), 0);
+  const bool lead = elect_one();
   bool ok = true;
-  bool pend_first = false;  // the tile whose PV is due is its segment's first
-  int pend_seg = 0;
-  // PV of tile j: every block's chunk is released by its own commit
-  auto pv = [&](int j, bool first, int sgi) {
-    ok = ok && x.wait(kPFull, j & 1, kSiteP);
-    if (first && sgi > 0) ok = ok && x.wait(kOFree, (sgi - 1) & 1, kSiteO);
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok) return;
-    tc_fence_after();
-    const uint64_t so = static_cast<uint64_t>((j & 1) * kStageBytes) >> 4;
+  uint32_t first = 0;  // bit i & 1: tile i is its segment's first
+  int v_seg = -1;      // segment of the last PV
+#pragma unroll 1
+  for (;;) {
+    if (o.pv_next()) {
+      const int i = o.v;
+      const bool fresh = (first >> (i & 1)) & 1u;
+      named_sync(kPReady, C::kSync);
+      if (fresh && ++v_seg > 0) ok = ok && x.wait(kOFree, (v_seg - 1) & 1, kSiteO);
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+      if (ok && lead) {
+        const uint64_t so = static_cast<uint64_t>((i & 1) * kStageBytes) >> 4;
+        const uint64_t bh = C::kSplitO ? dp : dph + so;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const uint32_t d = x.tmem + C::kTmemO + 64 * c;
-      const uint64_t av = dv + so + ((c * kChunkBytes) >> 4);
-      const uint64_t bh = C::kSplitO ? dp : dph + so;
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t d = C::kTmemO + 64 * c;
+          const uint64_t av = dv + so + ((c * kChunkBytes) >> 4);
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        mma_f8_ss_warp(d, av + ((kk * 4096) >> 4), bh + ((kk * 2048) >> 4), C::kIdescPV,
-                       kk > 0 || !first);
-      if constexpr (!C::kSplitO) {
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f8_ss(d, av + ((kk * 4096) >> 4), bh + ((kk * 2048) >> 4), C::kIdescPV,
+                           kk > 0 ? 1u : fresh ? 0u : 1u);
+          if constexpr (!C::kSplitO) {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_f8_ss_warp(d, av + ((kk * 4096) >> 4), dp + ((kk * 2048) >> 4), C::kIdescPV, 1u);
+            for (int kk = 0; kk < 4; ++kk)
+              mma_f8_ss(d, av + ((kk * 4096) >> 4), dp + ((kk * 2048) >> 4), C::kIdescPV, 1u);
+          }
+          mma_commit(x.bar(kEmpty + 5 * (i & 1) + c));  // each chunk goes as its block is done
+        }
+        mma_commit(x.bar(kEmpty + 5 * (i & 1) + 4));
+        mma_commit(x.bar(kPvDone));
       }
-      mma_commit_warp(x.bar + kEmpty + 5 * (j & 1) + c);
-    }
-    mma_commit_warp(x.bar + kEmpty + 5 * (j & 1) + 4);
-    mma_commit_warp(x.bar + kPvDone);
-  };
-  do {
-    for (int k = sg.k0; k < sg.k1 && ok; ++k, ++i) {
-      if (k == sg.k0) {
-        if (i > 0) pv(i - 1, pend_first, pend_seg);
-        ok = ok && x.wait(kQFull, seg & 1, kSiteQ);
-      }
-      if (i >= 2) ok = ok && x.wait(kSFree + (i & 1), ((i >> 1) - 1) & 1, kSiteSFree);
+      __syncwarp();
+      if (++o.v == o.n) break;
+    } else {
+      const int i = o.q, seg = o.seg;
+      const bool begins = o.begin_q(x, ok);
+      if (begins) ok = ok && x.wait(kQFull, seg & 1, kSiteQ);
+      first = (first & ~(1u << (i & 1))) | (begins ? 1u : 0u) << (i & 1);
+      if (i >= 2) named_sync(kSFree + (i & 1), C::kSync);
       const uint64_t so = static_cast<uint64_t>((i & 1) * kStageBytes) >> 4;
-      const uint32_t d = x.tmem + C::kTmemS + 2 * R * (i & 1);
+      const uint32_t d = C::kTmemS + 2 * R * (i & 1);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         ok = ok && x.wait(kFull + 5 * (i & 1) + c, (i >> 1) & 1, kSiteFull);
         ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
         tc_fence_after();
+        if (ok && lead) {
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          mma_f8_ss_warp(d, dk + so + ((c * kChunkBytes + ks * 32) >> 4),
-                         dq + ((c * C::kQChunk + ks * 32) >> 4), C::kIdescQK, c > 0 || ks > 0);
+          for (int ks = 0; ks < 4; ++ks)
+            mma_f8_ss(d, dk + so + ((c * kChunkBytes + ks * 32) >> 4),
+                           dq + ((c * C::kQChunk + ks * 32) >> 4), C::kIdescQK, c > 0 || ks > 0);
+        }
       }
       ok = ok && x.wait(kFull + 5 * (i & 1) + 4, (i >> 1) & 1, kSiteFull);
       ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
       tc_fence_after();
+      if (ok && lead) {
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks)
-        mma_f8_ss_warp(d, dkr + so + ((ks * 32) >> 4), dqr + ((ks * 32) >> 4), C::kIdescQK, 1u);
-      mma_commit_warp(x.bar + kSFull + (i & 1));
-      if (k > sg.k0) pv(i - 1, pend_first, pend_seg);
-      pend_first = k == sg.k0;
-      pend_seg = seg;
+        for (int ks = 0; ks < 2; ++ks)
+          mma_f8_ss(d, dkr + so + ((ks * 32) >> 4), dqr + ((ks * 32) >> 4), C::kIdescQK, 1u);
+        mma_commit(x.bar(kSFull + (i & 1)));
+      }
+      __syncwarp();
+      o.end_q();
     }
-    ++seg;
-  } while (ok && sg.next(a));
-  if (ok) pv(i - 1, pend_first, pend_seg);
+  }
   // every MMA has to be done before the tensor memory is released
-  mma_commit_warp(x.bar + kDrain);
-  drain_wait(x.bar + kDrain, 0);
+  if (lead) mma_commit(x.bar(kDrain));
+  __syncwarp();
+  drain_wait(x.bar(kDrain), 0);
 }
 
-// Softmax warps: warpgroup g takes the rows [g * HR, (g + 1) * HR), a thread
-// one key lane (then one dim lane of O). After a timeout they go on through
-// all tiles without waiting or storing (every wait returns at once then), so
-// that no warp is left alone at a named barrier.
+// Relay warp: sees the products done, in their order, and tells the softmax
+// warps. It tells them after a timeout, too (they never wait for anything else).
+template <int R>
+__device__ void relay(const Ctx<R>& x) {
+  using C = Cfg<R>;
+  Order<R> o;
+  o.n = static_cast<int>(x.ms()->n_tiles);
+  bool ok = true;
+#pragma unroll 1
+  for (;;) {
+    if (o.pv_next()) {
+      ok = ok && x.wait(kPvDone, o.v & 1, kSitePv);
+      __syncwarp();
+      // (with the softmax warps, not ahead of them: they have then taken note
+      // of the last S but one announced, whose barrier is the next one's)
+      named_sync(kPvReady, C::kSync);
+      if (++o.v == o.n) break;
+    } else {
+      const int i = o.q;
+      o.begin_q(x, ok);
+      if (i == 0) ok = ok && x.wait(kInfo, 0, kSiteInfo);
+      if (i + 1 < o.n) ok = ok && x.wait(kInfo + ((i + 1) & 3), ((i + 1) >> 2) & 1, kSiteInfo);
+      ok = ok && x.wait(kSFull + (i & 1), (i >> 1) & 1, kSiteSFull);
+      __syncwarp();
+      named_arrive(kSReady + (i & 1), C::kSync);
+      o.end_q();
+    }
+  }
+}
+
+// Two float32 in one 64-bit register: the FMA pipe takes pairs.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+  return v;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// Softmax warps: warpgroup g takes the rows [16 g, 16 g + 16), a thread one key
+// lane (then one dim lane of O). Four groups at R = 64 rather than two with 32
+// rows each: twice the warps to hide the latencies of a tile's chain (load,
+// vote, exp2, conversions), in as many registers. The rows' references and
+// factors are in lanes and come by shuffles, not from shared memory.
+// These warps wait for nothing but the hardware barriers, which the relay and
+// the MMA warp always reach, in any order of theirs: after a timeout all go
+// through the barriers of every tile, and nothing is stored.
 template <int R>
 __device__ void softmax_warps(const Ctx<R>& x) {
   using C = Cfg<R>;
-  constexpr int HR = C::HR;
   const CacheAttnArgs& a = x.p.a;
-  const int warp = (threadIdx.x >> 5) - kSoftmaxWarp0, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = warp >> 2, quarter = warp & 3, key = 32 * quarter + lane;
   const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
-  const int ps = a.cache.page_size;
-  float* s_m = reinterpret_cast<float*>(x.s + C::kOffM);      // [8][32]
-  float* my_m = s_m + 32 * warp;
-  float* rowfac = reinterpret_cast<float*>(x.s + C::kOffRow);
-  int* row_t = reinterpret_cast<int*>(rowfac + 64);
-  Segments<R> sg;
-  sg.begin(a, x.ms->slot, x.ms->k0, x.ms->n_tiles);
-  convert_q<R>(a, sg.it, x.s + C::kOffQ, rowfac, row_t);
-  fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) mbar_arrive(x.bar + kQFull);
-  named_sync(3, 256);
+  const int slot = key / a.cache.page_size;  // the key's page within a tile
+  float* s_m = reinterpret_cast<float*>(x.s() + C::kOffM);  // exchange between the warps of a group
+  float* my_m = s_m + HR * warp;
+  float* rowfac = reinterpret_cast<float*>(x.s() + C::kOffRow);
+  uint8_t* row_dt = reinterpret_cast<uint8_t*>(rowfac + 64);
+  const int n = static_cast<int>(x.ms()->n_tiles);
   int i = 0;
-  bool ok = true;
-  for (;;) {
-    const Item it = sg.it;
-    const int k0 = sg.k0, k1 = sg.k1;
-    float l[HR];
+  int e_page = 0, t0 = 0;
+  bool masked = false;
+  float l[HR];
+  float m = 0.f;  // lane r: the reference of row 16 g + r, an integer
+#pragma unroll 1
+  for (int seg = 0;; ++seg) {
+    const bool more = seg == 0 || x.segment(seg - 1)->more != 0;
+    bool lost = false;  // the segment was never published: a timeout
+    if (more) {
+      // the segment's Q, while the last PV of the one before runs (the first
+      // barrier: every warp is done with that one's factors)
+      lost = named_or(kAll, 32 * C::kWarps, !x.wait_segment(seg));
+      if (!lost) {
+        convert_q<R>(a, x.segment(seg)->it, x.s() + C::kOffQ, rowfac, row_dt);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(x.bar(kQFull));
+        named_sync(kAll, 32 * C::kWarps);
+      }
+    }
+    if (seg > 0) {
+      const Segment& sg = *x.segment(seg - 1);
+      const Item& it = sg.it;
+      named_sync(kPvReady, C::kSync);
+      const bool ok = *reinterpret_cast<volatile int*>(&x.ms()->abort_flag) == 0;
+      tc_fence_after();
+      // row sums over the key lanes
+      float sum = warp_transpose_sum(l);
+      if (lane < HR) my_m[lane] = sum;
+      named_sync(kVote + g, 128);
+      sum = 0.f;
+      if (lane < HR) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sum += s_m[HR * (4 * g + q) + lane];
+      }
+      named_sync(kVote + g, 128);
+      const int r0 = g * HR;
+      const bool whole_item = sg.k0 == 0 && sg.k1 == it.nt;
+      const int n_rows = ok ? it.n_rows - r0 : 0;  // rows to store
+      const int64_t part = 2ll * blockIdx.x + (sg.k0 == 0 ? 1 : 0);
+      if (quarter == 0 && lane < HR && lane < n_rows) {
+        if (whole_item) {
+          if (a.lse)
+            a.lse[static_cast<int64_t>(it.row) + r0 + lane] =
+                sum > 0.f ? (m + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+        } else {
+          x.p.part_ml[part * R + r0 + lane] = make_float2(sum > 0.f ? m : -INFINITY, sum);
+        }
+      }
+      const float inv = whole_item ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
+      const int row0 = it.row + r0;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        float o[HR];
+        {
+          uint32_t v[HR];
+          const uint32_t col = lanes + C::kTmemO + 64 * c + g * HR;
+          tmem_ld_32x32b_x16(col, v);
+          if constexpr (C::kSplitO) {
+            uint32_t w[HR];
+            tmem_ld_32x32b_x16(col + 32, w);
+            tmem_ld_wait();
+#pragma unroll
+            for (int r = 0; r < HR; ++r)
+              o[r] = fmaf(__uint_as_float(w[r]), 0.0625f, __uint_as_float(v[r])) *
+                     __shfl_sync(0xffffffffu, inv, r);
+          } else {
+            tmem_ld_wait();
+#pragma unroll
+            for (int r = 0; r < HR; ++r)
+              o[r] = __uint_as_float(v[r]) * __shfl_sync(0xffffffffu, inv, r);
+          }
+        }
+        const int dim = c * 128 + 32 * quarter + lane;
+        if (whole_item) {
+          // lanes pair up: the even one stores row r, the odd one row r + 1
+          const bool odd = lane & 1;
+          uint16_t* out = a.out + (static_cast<int64_t>(row0) + (odd ? 1 : 0)) * kDC + (dim & ~1);
+#pragma unroll
+          for (int r = 0; r < HR; r += 2) {
+            const float other = __shfl_xor_sync(0xffffffffu, odd ? o[r] : o[r + 1], 1);
+            const __nv_bfloat162 v = odd ? __floats2bfloat162_rn(other, o[r + 1])
+                                         : __floats2bfloat162_rn(o[r], other);
+            if (r + (odd ? 1 : 0) < n_rows) *reinterpret_cast<__nv_bfloat162*>(out + r * kDC) = v;
+          }
+        } else {
+          float* out = x.p.part_o + (part * R + r0) * kDC + dim;
+#pragma unroll
+          for (int r = 0; r < HR; ++r)
+            if (r < n_rows) out[r * kDC] = o[r];
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(x.bar(kOFree));
+    }
+    if (!more) break;
+    if (lost) {
+      for (; i < n; ++i) {
+        named_sync(kSReady + (i & 1), C::kSync);
+        if (i + 2 < n) named_arrive(kSFree + (i & 1), C::kSync);
+        named_arrive(kPReady, C::kSync);
+        named_sync(kPvReady, C::kSync);
+      }
+      break;
+    }
+    const int n_seg = x.segment(seg)->k1 - x.segment(seg)->k0;
 #pragma unroll
     for (int r = 0; r < HR; ++r) l[r] = 0.f;
-    float m = 0.f;  // lane r: the reference of row g * HR + r
-    uint32_t unset = HR == 32 ? 0xffffffffu : (1u << HR) - 1u;  // rows that saw no key yet
-    if (lane < HR) my_m[lane] = 0.f;
-    __syncwarp();
-    auto page_at = [&](int k) {
-      const int s = it.tile(k) * kKeys + key;
-      if (!it.seen(s)) return -1;
-      const int pg =
-          __ldg(a.batch.page_table + static_cast<int64_t>(it.b) * a.batch.max_pages + s / ps);
-      return pg >= 0 && pg < a.cache.n_pages ? pg : -1;
-    };
-    int page = page_at(k0);
-    float sc = page >= 0 ? __ldg(a.cache.scale + page) : 1.f;
-    for (int k = k0; k < k1; ++k, ++i) {
-      const int page_next = k + 1 < k1 ? page_at(k + 1) : -1;
-      const int s = it.tile(k) * kKeys + key;
-      const int e_key = scale_exp(sc);
-      const float sk = pow2f(e_key), inv_sk = pow2f(-e_key), ek = static_cast<float>(e_key);
-      // does every row see the whole tile?
-      const int t0 = it.tile(k) * kKeys;
-      const bool whole = t0 + kKeys - 1 <= it.t_lo &&
-                         (a.window == 0 || t0 > it.t_hi - a.window || t0 + kKeys <= a.n_sink);
-      const bool masked = !whole || __any_sync(0xffffffffu, page < 0);
-      ok = ok && x.wait(kSFull + (i & 1), (i >> 1) & 1, kSiteSFull);
-      __syncwarp();
+    m = 0.f;
+    uint32_t unset = (1u << HR) - 1u;                      // rows that saw no key yet
+    const float fac = rowfac[g * HR + (lane & (HR - 1))];  // lane r: the factor of row 16 g + r
+    if (i == 0) {
+      named_sync(kSReady, C::kSync);  // (tile 0)
+      e_page = x.info(0)->exp[slot];
+      t0 = x.info(0)->t0;
+      masked = x.info(0)->masked != 0;
+    }
+#pragma unroll 1
+    for (int k = 0; k < n_seg; ++k, ++i) {
+      if (i > 0) named_sync(kSReady + (i & 1), C::kSync);
       tc_fence_after();
-      float z[HR];
+      const int e_key = e_page == kNoPage ? 0 : e_page;
+      // y = z log2e + e_key - m: the exponents of p''
+      float y[HR];
       {
         uint32_t hi[HR], lo[HR];
-        const uint32_t col = x.tmem + lanes + C::kTmemS + 2 * R * (i & 1) + g * HR;
-        tmem_ld_cols<HR>(col, hi);
-        tmem_ld_cols<HR>(col + R, lo);
+        const uint32_t col = lanes + C::kTmemS + 2 * R * (i & 1) + g * HR;
+        tmem_ld_32x32b_x16(col, hi);
+        tmem_ld_32x32b_x16(col + R, lo);
+        const float sk = pow2f(e_key), ek = static_cast<float>(e_key);
+        const uint64_t sk2 = pack2(sk, sk), ek2 = pack2(ek, ek), lo2 = pack2(0.0625f, 0.0625f),
+                       neg2 = pack2(-1.f, -1.f);
         tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(x.bar + kSFree + (i & 1));
+        if (i + 2 < n) named_arrive(kSFree + (i & 1), C::kSync);
 #pragma unroll
-        for (int r = 0; r < HR; ++r)
-          z[r] = fmaf(fmaf(__uint_as_float(lo[r]), 0.0625f, __uint_as_float(hi[r])),
-                      rowfac[g * HR + r] * sk, ek);
+        for (int j = 0; j < HR; j += 2) {
+          const uint64_t t = fma2(pack2(__uint_as_float(lo[j]), __uint_as_float(lo[j + 1])), lo2,
+                                  pack2(__uint_as_float(hi[j]), __uint_as_float(hi[j + 1])));
+          const uint64_t f = pack2(__shfl_sync(0xffffffffu, fac, j), __shfl_sync(0xffffffffu, fac, j + 1));
+          const uint64_t mm = pack2(__shfl_sync(0xffffffffu, m, j), __shfl_sync(0xffffffffu, m, j + 1));
+          const float2 v = unpack2(fma2(t, mul2(f, sk2), fma2(mm, neg2, ek2)));
+          y[j] = v.x;
+          y[j + 1] = v.y;
+        }
       }
+      bool gone = false;  // no row sees this lane's key, or it has no page
       if (masked) {
+        const Item& it = x.segment(seg)->it;
+        const int s = t0 + key;
+        gone = e_page == kNoPage || !it.seen(s);
         // row at position t sees key s iff s <= t and (t < s + window or s < n_sink)
-        const unsigned span = page < 0 ? 0u
+        const unsigned span = gone ? 0u
                               : a.window == 0 || s < a.n_sink ? 0x7fffffffu
                                                               : static_cast<unsigned>(a.window);
+        const int dt = it.t_lo - s;
 #pragma unroll
         for (int r = 0; r < HR; ++r)
-          if (static_cast<unsigned>(row_t[g * HR + r] - s) >= span) z[r] = -INFINITY;
+          if (static_cast<unsigned>(dt + row_dt[g * HR + r]) >= span) y[r] = -INFINITY;
       }
-      float over = -INFINITY;
+      float over = y[0];
 #pragma unroll
-      for (int r = 0; r < HR; ++r) over = fmaxf(over, z[r] - my_m[r]);
-      bool pv_waited = i == 0;
-      if (named_or(1 + g, 128, over > 8.f) || unset != 0u) {
+      for (int r = 1; r < HR; ++r) over = fmaxf(over, y[r]);
+      bool pv_due = k > 0;  // the previous PV has to be waited for (a segment's last one was)
+      if (named_or(kVote + g, 128, over > 8.f) || unset != 0u) {
         // a new reference for the rows that need one
         float mx = -INFINITY;
 #pragma unroll
         for (int r = 0; r < HR; ++r) {
-          const float v = warp_max(z[r]);
+          const float v = warp_max(y[r]);
           if (lane == r) mx = v;
         }
-        __syncwarp();
         if (lane < HR) my_m[lane] = mx;
-        named_sync(1 + g, 128);
+        named_sync(kVote + g, 128);
         if (lane < HR) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) mx = fmaxf(mx, s_m[32 * (4 * g + q) + lane]);
+          for (int q = 0; q < 4; ++q) mx = fmaxf(mx, s_m[HR * (4 * g + q) + lane]);
         }
-        named_sync(1 + g, 128);
+        named_sync(kVote + g, 128);
         const bool fresh = (unset >> lane) & 1u;
-        const bool up = lane < HR && (fresh ? mx > -INFINITY : mx - m > 8.f);
-        const float m_new = up ? ceilf(mx) - 6.f : m;
-        const float f = up && !fresh ? ex2_approx(m - m_new) : 1.f;
+        const bool up = lane < HR && (fresh ? mx > -INFINITY : mx > 8.f);
+        const float d = up ? ceilf(mx) - 6.f : 0.f;  // what the reference rises by
+        const float f = up && !fresh ? ex2_approx(-d) : 1.f;
         unset &= ~__ballot_sync(0xffffffffu, up);
-        m = m_new;
-        if (lane < HR) my_m[lane] = m;
-        __syncwarp();
+        m += d;
+#pragma unroll
+        for (int r = 0; r < HR; ++r) y[r] -= __shfl_sync(0xffffffffu, d, r);
         if (__any_sync(0xffffffffu, f != 1.f)) {
-          if (i > 0) ok = ok && x.wait(kPvDone, (i - 1) & 1, kSitePv);
-          __syncwarp();
-          pv_waited = true;
+          if (pv_due) named_sync(kPvReady, C::kSync);
           tc_fence_after();
           float fr[HR];
 #pragma unroll
@@ -720,33 +1054,31 @@ __device__ void softmax_warps(const Ctx<R>& x) {
             fr[r] = __shfl_sync(0xffffffffu, f, r);
             l[r] *= fr[r];
           }
-          if (k > k0) {
-#pragma unroll
+          if (pv_due) {
+#pragma unroll 1
             for (int c = 0; c < (C::kSplitO ? 8 : 4); ++c) {
-              const uint32_t col = x.tmem + lanes + C::kTmemO + (C::kSplitO ? 32 : 64) * c + g * HR;
+              const uint32_t col = lanes + C::kTmemO + (C::kSplitO ? 32 : 64) * c + g * HR;
               uint32_t o[HR];
-              tmem_ld_cols<HR>(col, o);
+              tmem_ld_32x32b_x16(col, o);
               tmem_ld_wait();
 #pragma unroll
               for (int r = 0; r < HR; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * fr[r]);
-              tmem_st_cols<HR>(col, o);
+              tmem_st_32x32b_x16(col, o);
             }
             tmem_st_wait();
           }
+          pv_due = false;
         }
       }
-      if (!pv_waited) {  // P's place is free once the previous PV is done
-        ok = ok && x.wait(kPvDone, (i - 1) & 1, kSitePv);
-      }
-      unsigned char* stage = x.s + C::kOffStage + (i & 1) * kStageBytes;
+      uint32_t hi[HR / 4], lo[HR / 4];
       {
-        uint32_t hi[HR / 4], lo[HR / 4];
+        const float inv_sk = pow2f(-e_key);
 #pragma unroll
         for (int r = 0; r < HR; r += 4) {
           float p[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            p[e] = ex2_approx(z[r + e] - my_m[r + e]);
+            p[e] = ex2_approx(y[r + e]);
             l[r + e] = fmaf(p[e], inv_sk, l[r + e]);
           }
           const uint32_t h0 = f32_to_e4m3x2(p[0], p[1]), h1 = f32_to_e4m3x2(p[2], p[3]);
@@ -756,187 +1088,92 @@ __device__ void softmax_warps(const Ctx<R>& x) {
           lo[r / 4] = f32_to_e4m3x2((p[0] - b0.x) * kLo, (p[1] - b0.y) * kLo) |
                       f32_to_e4m3x2((p[2] - b1.x) * kLo, (p[3] - b1.y) * kLo) << 16;
         }
-        unsigned char* row_hi = (C::kSplitO ? x.s + C::kOffP : stage + kRopeOff) + key * 64;
-        unsigned char* row_lo = x.s + C::kOffP + key * 64;
-        const int sw = (key >> 1) & 3;
-#pragma unroll
-        for (int u = 0; u < HR / 16; ++u) {
-          const int uh = g * (HR / 16) + u, ul = C::kSplitO ? 2 + g : uh;
-          *reinterpret_cast<uint4*>(row_hi + ((uh ^ sw) << 4)) =
-              make_uint4(hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
-          *reinterpret_cast<uint4*>(row_lo + ((ul ^ sw) << 4)) =
-              make_uint4(lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
-        }
       }
-      if (masked) {
+      if (pv_due) named_sync(kPvReady, C::kSync);  // P's place is free
+      unsigned char* stage = x.s() + C::kOffStage + (i & 1) * kStageBytes;
+      {
+        // 16 rows are one 16-byte unit of the key's 64-byte row, 64-byte swizzle
+        unsigned char* row_hi = (C::kSplitO ? x.s() + C::kOffP : stage + kRopeOff) + key * 64;
+        unsigned char* row_lo = x.s() + C::kOffP + key * 64;
+        const int sw = (key >> 1) & 3, ul = C::kSplitO ? 2 + g : g;
+        *reinterpret_cast<uint4*>(row_hi + ((g ^ sw) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(row_lo + ((ul ^ sw) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+      if (__any_sync(0xffffffffu, gone)) {
         // A key that no row sees: its bytes may be anything, and 0 * NaN is
         // NaN, so its latent row is zeroed before the PV. The tile's chunks
         // have landed (QK^T read them); waiting on them orders the writes.
-        for (int c = 0; c < 4; ++c) ok = ok && x.wait(kFull + 5 * (i & 1) + c, (i >> 1) & 1, kSiteFull);
-        if (page < 0) {
-#pragma unroll
-          for (int c = 2 * g; c < 2 * g + 2; ++c)
+#pragma unroll 1
+        for (int c = g; c < 4; c += C::kGroups) {
+          const bool there = x.wait(kFull + 5 * (i & 1) + c, (i >> 1) & 1, kSiteFull);
+          if (gone && there) {
+            // (lanes start at different units, for different banks)
 #pragma unroll
             for (int u = 0; u < 8; ++u)
-              *reinterpret_cast<uint4*>(stage + c * kChunkBytes + key * 128 + u * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
+              *reinterpret_cast<uint4*>(stage + c * kChunkBytes + key * 128 +
+                                        (((u + lane) & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+          }
         }
       }
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(x.bar + kPFull);
-      page = page_next;
-      sc = page >= 0 ? __ldg(a.cache.scale + page) : 1.f;
-    }
-    // the next segment's Q, while the last PV runs
-    const bool more = sg.next(a);
-    if (more) {
-      named_sync(3, 256);  // every warp is done with this item's factors
-      convert_q<R>(a, sg.it, x.s + C::kOffQ, rowfac, row_t);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(x.bar + kQFull);
-      named_sync(3, 256);
-    }
-    ok = ok && x.wait(kPvDone, (i - 1) & 1, kSitePv);
-    ok = __all_sync(0xffffffffu, ok);
-    tc_fence_after();
-    // row sums over the key lanes
-    float sum = warp_transpose_sum<HR>(l);
-    __syncwarp();
-    if (lane < HR) my_m[lane] = sum;
-    named_sync(1 + g, 128);
-    sum = 0.f;
-    if (lane < HR) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) sum += s_m[32 * (4 * g + q) + lane];
-    }
-    named_sync(1 + g, 128);
-    const int r0 = g * HR;
-    const bool whole_item = k0 == 0 && k1 == it.nt;
-    const int64_t part = 2ll * blockIdx.x + (k0 == 0 ? 1 : 0);
-    if (ok && quarter == 0 && lane < HR && r0 + lane < it.n_rows) {
-      if (whole_item) {
-        if (a.lse)
-          a.lse[static_cast<int64_t>(it.row) + r0 + lane] =
-              sum > 0.f ? (m + log2f(sum)) * 0.69314718055994531f : -INFINITY;
-      } else {
-        x.p.part_ml[part * R + r0 + lane] = make_float2(sum > 0.f ? m : -INFINITY, sum);
+      named_arrive(kPReady, C::kSync);
+      if (i + 1 < n) {
+        const TileInfo* next = x.info(i + 1);
+        e_page = next->exp[slot];
+        t0 = next->t0;
+        masked = next->masked != 0;
       }
     }
-    if (lane < HR) my_m[lane] = whole_item ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
-    __syncwarp();
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      float o[HR];
-      {
-        uint32_t v[HR];
-        const uint32_t col = x.tmem + lanes + C::kTmemO + 64 * c + g * HR;
-        tmem_ld_cols<HR>(col, v);
-        if constexpr (C::kSplitO) {
-          uint32_t w[HR];
-          tmem_ld_cols<HR>(col + 32, w);
-          tmem_ld_wait();
-#pragma unroll
-          for (int r = 0; r < HR; ++r)
-            o[r] = fmaf(__uint_as_float(w[r]), 0.0625f, __uint_as_float(v[r])) * my_m[r];
-        } else {
-          tmem_ld_wait();
-#pragma unroll
-          for (int r = 0; r < HR; ++r) o[r] = __uint_as_float(v[r]) * my_m[r];
-        }
-      }
-      const int dim = c * 128 + 32 * quarter + lane;
-      if (whole_item) {
-        // lanes pair up: the even one stores row r, the odd one row r + 1
-        uint16_t* out = a.out + (static_cast<int64_t>(it.row) + r0) * kDC + (dim & ~1);
-        const bool odd = lane & 1;
-#pragma unroll
-        for (int r = 0; r < HR; r += 2) {
-          const float other = __shfl_xor_sync(0xffffffffu, odd ? o[r] : o[r + 1], 1);
-          const __nv_bfloat162 v = odd ? __floats2bfloat162_rn(other, o[r + 1])
-                                       : __floats2bfloat162_rn(o[r], other);
-          const int row = r + (odd ? 1 : 0);
-          if (ok && r0 + row < it.n_rows)
-            *reinterpret_cast<__nv_bfloat162*>(out + static_cast<int64_t>(row) * kDC) = v;
-        }
-      } else {
-        float* out = x.p.part_o + (part * R + r0) * kDC + dim;
-#pragma unroll
-        for (int r = 0; r < HR; ++r)
-          if (ok && r0 + r < it.n_rows) out[static_cast<int64_t>(r) * kDC] = o[r];
-      }
-    }
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(x.bar + kOFree);
-    if (!more) break;
   }
 }
 
 template <int R>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<R>::kThreads, 1)
     cache_attn_tc(const __grid_constant__ CacheAttnParams p, const __grid_constant__ CUtensorMap ml,
                   const __grid_constant__ CUtensorMap mr) {
   using C = Cfg<R>;
-  extern __shared__ unsigned char smem_raw[];
-  Ctx<R> x{p};
-  x.s = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                         ~static_cast<uintptr_t>(1023));
-  x.bar = reinterpret_cast<uint64_t*>(x.s + C::kOffBar);
-  x.ms = reinterpret_cast<Misc*>(x.s + C::kOffMisc);
+  const Ctx<R> x{p};
+  Misc* ms = x.ms();
   const int tid = threadIdx.x, warp = tid >> 5;
   if (tid == 0) {
-    x.ms->status = x.ms->info = 0u;
-    x.ms->abort_flag = 0;
-    for (int b = 0; b < C::kNumBars; ++b) {
-      const bool by_warps = b == kSFree || b == kSFree + 1 || b == kPFull || b == kQFull || b == kOFree;
-      mbar_init(x.bar + b, by_warps ? 8 : 1);
-    }
+    ms->status = ms->info = 0u;
+    ms->abort_flag = 0;
+    for (int b = 0; b < C::kNumBars; ++b)
+      mbar_init(x.bar(b), b == kQFull || b == kOFree ? C::kWarps : 1);
     fence_barrier_init();
     prefetch_tmap(&ml);
     prefetch_tmap(&mr);
   }
-  if (warp == 1) tmem_alloc(&x.ms->tmem, 512);
-  schedule<R>(p.a, x.ms);  // ends with a barrier
+  if (warp == C::kWarps + 1) tmem_alloc(&ms->tmem, 512);
+  __syncthreads();  // the status word before schedule() may report
+  schedule<R>(p.a, ms, reinterpret_cast<long long*>(x.s() + C::kOffM));  // ends with a barrier
   tc_fence_after();
-  x.tmem = x.ms->tmem;
-  if (blockIdx.x == 0)  // the batch arrays, once for all
-    for (int b = tid; b < p.a.batch.n_seq; b += kThreads)
-      if (!seq_range(p.a.batch, p.a.cache.page_size, b).ok) x.error(kCacheSiteSeq);
-  const bool work = x.ms->n_tiles > 0;
+  // All 512 columns are this CTA's, so they begin at 0; operands are at
+  // constant addresses on that account.
+  bool work = ms->n_tiles > 0;
+  if (ms->tmem != 0u || (smem_u32(x.s()) & 1023u) != 0u) {
+    if (tid == 0) report(reinterpret_cast<WsHeader*>(&ms->status), kDevInternal, 0);
+    work = false;
+  }
   if (work) {
-    if (warp == 0) producer<R>(x, &ml, &mr);
-    else if (warp == 1) mma_issuer<R>(x);
-    else if (warp >= kSoftmaxWarp0) softmax_warps<R>(x);
+    if (warp < C::kWarps) softmax_warps<R>(x);
+    else if (warp == C::kWarps) producer<R>(x, &ml, &mr);
+    else if (warp == C::kWarps + 1) mma_issuer<R>(x);
+    else relay<R>(x);
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == C::kWarps + 1) {
     tc_fence_after();
-    tmem_dealloc(x.tmem, 512);
+    tmem_dealloc(ms->tmem, 512);
   }
   if (tid == 0) {
-    CtaMeta me;
-    me.status = x.ms->status;
-    me.info = x.ms->info;
-    me.row = me.n_rows = me.first = 0;
-    if (work && x.ms->k0 > 0) {
-      // the first segment's item began in another CTA; does it end here?
-      ItemWalk<R> w;
-      Item it;
-      w.seek(p.a, x.ms->slot);
-      w.item(p.a, it);
-      if (x.ms->k0 + x.ms->n_tiles >= it.nt) {
-        const long long g = min(static_cast<long long>(gridDim.x), x.ms->total);
-        const long long begin = x.ms->total * blockIdx.x / g;
-        me.row = it.row;
-        me.n_rows = it.n_rows;
-        me.first = cta_of_tile(begin - x.ms->k0, x.ms->total, gridDim.x);
-      }
-    }
-    p.meta[blockIdx.x] = me;
+    CtaMeta& me = p.meta[blockIdx.x];
+    me.status = ms->status;
+    me.info = ms->info;
+    if (!work) me.n_rows = 0;
   }
 }
 
@@ -1189,7 +1426,7 @@ cudaError_t launch_tc(const CacheAttnArgs& a, void* scratch, cudaStream_t st) {
   p.part_ml = reinterpret_cast<float2*>(w);
   w += kMaxCtas * 2 * R * sizeof(float2);
   p.part_o = reinterpret_cast<float*>(w);
-  cache_attn_tc<R><<<grid, kThreads, Cfg<R>::kSmemBytes, st>>>(p, ml, mr);
+  cache_attn_tc<R><<<grid, Cfg<R>::kThreads, Cfg<R>::kSmemBytes, st>>>(p, ml, mr);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cache_attn_combine<R><<<grid, kCombineThreads, 0, st>>>(p, grid);

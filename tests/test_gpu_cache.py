@@ -402,6 +402,15 @@ def test_attn_long_context_over_many_sms(dsa):
     run_attn(dsa, Setup([9000], [3], page=64, heads=16, seed=17), window=6000, n_sink=300)
 
 
+@pytest.mark.parametrize("window,n_sink", [(0, 0), (200, 4)])
+@pytest.mark.parametrize("lens,new,heads", [([700, 1300], [300, 40], 32), ([520] * 90, [1] * 90, 32),
+                                            ([900, 40, 1500], [128, 40, 3], 128)])
+def test_attn_sms_that_take_several_sequences(dsa, lens, new, heads, window, n_sink):
+    """More tiles than SMs: an SM goes through parts of several items, each of
+    several tiles, with whole items between the parts that cross SMs."""
+    run_attn(dsa, Setup(lens, new, heads=heads, page=32, seed=26), window, n_sink)
+
+
 def test_attn_shared_prefix_page(dsa):
     run_attn(dsa, Setup([200, 90, 300], [2, 1, 1], seed=18, shared=True))
 
