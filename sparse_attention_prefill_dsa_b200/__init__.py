@@ -399,13 +399,37 @@ def _ld(ld, x, dim, default):
         return int(ld)
     if x is None or isinstance(x, int):
         return default
-    if x.shape[-1] > 1 and x.stride(-1) != 1:
+    strides = x.stride()
+    if strides[-1] != 1 and x.shape[-1] > 1:
         raise ValueError("rows have to be dense in their last dimension")
-    return x.stride(dim) if x.shape[dim] > 1 else default
+    return strides[dim] if x.shape[dim] > 1 else default
 
 
 def dsa_cache_workspace_size(cache, batch, n_heads: int) -> int:
     return int(library().dsa_cache_workspace_size(cache, batch, int(n_heads)))
+
+
+def _at(x):
+    """Address of a tensor or raw address (ctypes converts the int)."""
+    return x if x is None or isinstance(x, int) else x.data_ptr()
+
+
+_raw_stream = None
+
+
+def _on(stream):
+    """Raw stream: the one given, or torch's current one, without making a
+    torch.cuda.Stream for it (these calls are made every step of a decode)."""
+    global _raw_stream
+    if stream is not None:
+        return stream if isinstance(stream, int) else stream.cuda_stream
+    if _raw_stream is None:
+        import torch
+
+        get, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
+        _raw_stream = (lambda: get(device())) if get is not None else (
+            lambda: torch.cuda.current_stream().cuda_stream)
+    return _raw_stream()
 
 
 def dsa_cache_append(cache, batch, latent, rope, inv_freq, rope_style, q_rope, q, n_heads,
@@ -414,21 +438,21 @@ def dsa_cache_append(cache, batch, latent, rope, inv_freq, rope_style, q_rope, q
     """Strides are taken from the tensors unless given (see include/dsa.h)."""
     dr = cache.d_rope
     return library().dsa_cache_append(
-        cache, batch, _p(latent), _ld(ld_latent, latent, 0, cache.d_latent), _p(rope),
-        _ld(ld_rope, rope, 0, dr), _p(inv_freq), int(rope_style), _p(q_rope),
-        _ld(ld_q_tok, q_rope, 0, n_heads * dr), _ld(ld_q_head, q_rope, 1, dr), _p(q), int(n_heads),
-        _p(workspace), _nbytes(workspace, workspace_bytes), _stream(stream))
+        cache, batch, _at(latent), _ld(ld_latent, latent, 0, cache.d_latent), _at(rope),
+        _ld(ld_rope, rope, 0, dr), _at(inv_freq), rope_style, _at(q_rope),
+        _ld(ld_q_tok, q_rope, 0, n_heads * dr), _ld(ld_q_head, q_rope, 1, dr), _at(q), n_heads,
+        _at(workspace), _nbytes(workspace, workspace_bytes), _on(stream))
 
 
 def dsa_cache_gather(cache, batch, seq, pos0, n_rows, latent, rope, workspace,
                      workspace_bytes=None, stream=None) -> int:
-    return library().dsa_cache_gather(cache, batch, int(seq), int(pos0), int(n_rows), _p(latent),
-                                      _p(rope), _p(workspace), _nbytes(workspace, workspace_bytes),
-                                      _stream(stream))
+    return library().dsa_cache_gather(cache, batch, seq, pos0, n_rows, _at(latent), _at(rope),
+                                      _at(workspace), _nbytes(workspace, workspace_bytes),
+                                      _on(stream))
 
 
 def dsa_cache_attn(cache, batch, q, n_heads, softmax_scale, window, n_sink, out, lse, workspace,
                    workspace_bytes=None, stream=None) -> int:
-    return library().dsa_cache_attn(cache, batch, _p(q), int(n_heads), float(softmax_scale),
-                                    int(window), int(n_sink), _p(out), _p(lse), _p(workspace),
-                                    _nbytes(workspace, workspace_bytes), _stream(stream))
+    return library().dsa_cache_attn(cache, batch, _at(q), n_heads, softmax_scale, window, n_sink,
+                                    _at(out), _at(lse), _at(workspace),
+                                    _nbytes(workspace, workspace_bytes), _on(stream))

@@ -26,8 +26,6 @@
 namespace dsa {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kQTokens = 4;  // tokens of a q CTA
 
 // ------------------------------------------------------------------ status
 
@@ -116,22 +114,43 @@ __device__ void rescale_codes(uint8_t* p, int n16, float f) {
 }
 
 // Sixteen-byte units of a latent row (8 elements) and pairs of a rope row are
-// dealt over the CTA so that each thread holds kUnits and kPairs of them.
+// dealt over the CTA so that each thread holds kUnits and kPairs of them: at
+// most eight and four, in 64 registers, so that an SM runs 1,024 threads (with
+// 256 threads a page of 64 they took 128, and a chunk of 8,192 tokens 33 us).
 template <int DC, int DR, int PS>
 struct AppendCfg {
-  static constexpr int kThr = PS == 128 ? 2 * kThreads : kThreads;
+  static constexpr int kThr = PS <= 32 ? 256 : 8 * PS;
+  static constexpr int kMinBlocks = 1024 / kThr;
+  static constexpr int kQTokens = kThr / 64;  // tokens of a q CTA
   static constexpr int kRowUnits = DC / 8;
   static constexpr int kUnits = (PS * kRowUnits + kThr - 1) / kThr;
   static constexpr int kRowPairs = DR / 2;
   static constexpr int kPairs = (PS * kRowPairs + kThr - 1) / kThr;
 };
 
+// seq_of_slot by the whole block: every step loads one start a thread and
+// counts those up to the slot, so that up to as many sequences as threads take
+// one load instead of a chain of log2 of them.
+__device__ int block_seq_of_slot(const dsa_batch& bt, int64_t slot, int shift, int extra) {
+  int lo = 0, n = bt.n_seq;  // the answer is one of lo .. lo + n - 1
+  while (n > 1) {
+    const int step = (n + blockDim.x - 1) / blockDim.x;
+    const int64_t k = static_cast<int64_t>(threadIdx.x) * step;
+    const int count =
+        __syncthreads_count(k < n && slot_start(bt, lo + static_cast<int>(k), 1, shift, extra) <= slot);
+    const int at = max(count - 1, 0) * step;
+    lo += at;
+    n = min(step, n - at);
+  }
+  return lo;
+}
+
 template <int DC, int DR, int PS>
 __device__ void append_page(const AppendArgs& a, int64_t slot) {
   using C = AppendCfg<DC, DR, PS>;
   __shared__ int s_exp;
   constexpr int kShift = PS == 16 ? 4 : PS == 32 ? 5 : PS == 64 ? 6 : 7;
-  const int b = seq_of_slot(a.batch, slot, 1, kShift, 2);
+  const int b = block_seq_of_slot(a.batch, slot, kShift, 2);
   const SeqRange r = seq_range(a.batch, PS, b);
   const int64_t j = slot - slot_start(a.batch, b, 1, kShift, 2);
   if (r.n == 0 || j < 0) return;
@@ -233,12 +252,67 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float x, float y) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Rotates the queries' rope of kQTokens tokens. A work item is eight pairs of
-// one head: two 16-byte groups, adjacent (interleaved) or d_rope/2 apart.
+// Eight pairs of one head: two 16-byte groups, adjacent (interleaved) or
+// d_rope/2 apart.
 template <int DC, int DR>
+struct QItem {
+  uint4 v, w;
+  const uint4* src;
+  uint4* dst;
+  const float2* cs;
+  int other;  // groups between the two
+  __device__ __forceinline__ bool load(const AppendArgs& a, int64_t tok0, int x, int items,
+                                       const float2* s_cs) {
+    if (x >= items) return false;
+    constexpr int kPerHead = DR / 16;
+    const int g = x % kPerHead, h = (x / kPerHead) % a.n_heads, k = x / kPerHead / a.n_heads;
+    const int64_t tok = tok0 + k;
+    if (tok >= a.batch.n_tok) return false;
+    other = a.halves ? DR / 16 : 1;
+    const int at = a.halves ? g : 2 * g;
+    src = reinterpret_cast<const uint4*>(a.q_rope + tok * a.ld_q_tok + h * a.ld_q_head) + at;
+    dst = reinterpret_cast<uint4*>(a.q + (tok * a.n_heads + h) * (DC + DR) + DC) + at;
+    cs = s_cs + k * (DR / 2) + g * 8;
+    v = __ldg(src);
+    w = __ldg(src + other);
+    return true;
+  }
+  __device__ __forceinline__ void store(bool halves) const {
+    const uint32_t vi[4] = {v.x, v.y, v.z, v.w}, wi[4] = {w.x, w.y, w.z, w.w};
+    uint32_t vo[4], wo[4];
+    if (halves) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 p = bf16x2(vi[e]), q = bf16x2(wi[e]), c0 = cs[2 * e], c1 = cs[2 * e + 1];
+        vo[e] = pack_bf16x2(p.x * c0.x - q.x * c0.y, p.y * c1.x - q.y * c1.y);
+        wo[e] = pack_bf16x2(q.x * c0.x + p.x * c0.y, q.y * c1.x + p.y * c1.y);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 p = bf16x2(vi[e]), q = bf16x2(wi[e]), c0 = cs[e], c1 = cs[4 + e];
+        vo[e] = pack_bf16x2(p.x * c0.x - p.y * c0.y, p.y * c0.x + p.x * c0.y);
+        wo[e] = pack_bf16x2(q.x * c1.x - q.y * c1.y, q.y * c1.x + q.x * c1.y);
+      }
+    }
+    dst[0] = make_uint4(vo[0], vo[1], vo[2], vo[3]);
+    dst[other] = make_uint4(wo[0], wo[1], wo[2], wo[3]);
+  }
+};
+
+// Rotates the queries' rope of kQTokens tokens. A thread's first items are
+// loaded before the angles are worked out.
+template <int DC, int DR, int kQTokens>
 __device__ void rotate_q(const AppendArgs& a, int64_t tok0) {
-  __shared__ float2 s_cs[kQTokens][DR / 2];
+  __shared__ float2 s_cs[kQTokens * (DR / 2)];
   __shared__ int s_pos[kQTokens];
+  constexpr int kPerHead = DR / 16, kAhead = 2;
+  const int items = kQTokens * a.n_heads * kPerHead;
+  QItem<DC, DR> it[kAhead];
+  bool has[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i)
+    has[i] = it[i].load(a, tok0, threadIdx.x + i * blockDim.x, items, s_cs);
   if (threadIdx.x < kQTokens) {
     const int64_t tok = tok0 + threadIdx.x;
     int pos = -1;
@@ -253,60 +327,34 @@ __device__ void rotate_q(const AppendArgs& a, int64_t tok0) {
   }
   __syncthreads();
   for (int x = threadIdx.x; x < kQTokens * (DR / 2); x += blockDim.x) {
-    const int k = x / (DR / 2), i = x % (DR / 2);
     double sn, cs;
-    sincos(static_cast<double>(s_pos[k]) * static_cast<double>(__ldg(a.inv_freq + i)), &sn, &cs);
-    s_cs[k][i] = make_float2(static_cast<float>(cs), static_cast<float>(sn));
+    sincos(static_cast<double>(s_pos[x / (DR / 2)]) *
+               static_cast<double>(__ldg(a.inv_freq + x % (DR / 2))), &sn, &cs);
+    s_cs[x] = make_float2(static_cast<float>(cs), static_cast<float>(sn));
   }
   __syncthreads();
-  const int per_head = DR / 16, items = kQTokens * a.n_heads * per_head;
-  for (int x = threadIdx.x; x < items; x += blockDim.x) {
-    const int g = x % per_head, h = (x / per_head) % a.n_heads, k = x / per_head / a.n_heads;
-    if (s_pos[k] < 0) continue;
-    const int64_t tok = tok0 + k;
-    const uint4* src = reinterpret_cast<const uint4*>(a.q_rope + tok * a.ld_q_tok + h * a.ld_q_head);
-    uint4* dst = reinterpret_cast<uint4*>(a.q + (tok * a.n_heads + h) * (DC + DR) + DC);
-    const float2* cs = &s_cs[k][g * 8];
-    if (a.halves) {
-      const uint4 v = __ldg(src + g), w = __ldg(src + g + DR / 16);
-      const uint32_t vi[4] = {v.x, v.y, v.z, v.w}, wi[4] = {w.x, w.y, w.z, w.w};
-      uint32_t vo[4], wo[4];
+  for (int x = threadIdx.x; x < items; x += kAhead * blockDim.x) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 p = bf16x2(vi[e]), q = bf16x2(wi[e]), c0 = cs[2 * e], c1 = cs[2 * e + 1];
-        vo[e] = pack_bf16x2(p.x * c0.x - q.x * c0.y, p.y * c1.x - q.y * c1.y);
-        wo[e] = pack_bf16x2(q.x * c0.x + p.x * c0.y, q.y * c1.x + p.y * c1.y);
-      }
-      dst[g] = make_uint4(vo[0], vo[1], vo[2], vo[3]);
-      dst[g + DR / 16] = make_uint4(wo[0], wo[1], wo[2], wo[3]);
-    } else {
+    for (int i = 0; i < kAhead; ++i)
+      if (has[i] && s_pos[(x + i * blockDim.x) / (kPerHead * a.n_heads)] >= 0) it[i].store(a.halves);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const uint4 v = __ldg(src + 2 * g + half);
-        const uint32_t vi[4] = {v.x, v.y, v.z, v.w};
-        uint32_t vo[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 p = bf16x2(vi[e]), c = cs[4 * half + e];
-          vo[e] = pack_bf16x2(p.x * c.x - p.y * c.y, p.y * c.x + p.x * c.y);
-        }
-        dst[2 * g + half] = make_uint4(vo[0], vo[1], vo[2], vo[3]);
-      }
-    }
+    for (int i = 0; i < kAhead; ++i)
+      has[i] = it[i].load(a, tok0, x + (kAhead + i) * blockDim.x, items, s_cs);
   }
 }
 
 template <int DC, int DR, int PS>
-__global__ void __launch_bounds__(AppendCfg<DC, DR, PS>::kThr)
+__global__ void __launch_bounds__(AppendCfg<DC, DR, PS>::kThr, AppendCfg<DC, DR, PS>::kMinBlocks)
     cache_append_kernel(const __grid_constant__ AppendArgs a, int64_t page_slots) {
   const int64_t x = blockIdx.x;
   if (x < page_slots) append_page<DC, DR, PS>(a, x);
   else if (x == page_slots) append_check(a);
-  else rotate_q<DC, DR>(a, (x - page_slots - 1) * kQTokens);
+  else rotate_q<DC, DR, AppendCfg<DC, DR, PS>::kQTokens>(a, (x - page_slots - 1) * AppendCfg<DC, DR, PS>::kQTokens);
 }
 
 template <int DC, int DR, int PS>
 cudaError_t launch_append_t(const AppendArgs& a, cudaStream_t st) {
+  constexpr int kQTokens = AppendCfg<DC, DR, PS>::kQTokens;
   const int64_t pages = a.batch.n_tok / PS + 2ll * a.batch.n_seq;
   const int64_t q = a.q ? (static_cast<int64_t>(a.batch.n_tok) + kQTokens - 1) / kQTokens : 0;
   cache_append_kernel<DC, DR, PS><<<static_cast<unsigned>(pages + 1 + q),
@@ -332,65 +380,91 @@ struct GatherArgs {
   uint16_t* latent;
   uint16_t* rope;
   int seq, pos0, n_rows;
+  bool wide;  // both outputs on 32-byte boundaries
   WsHeader* ws;
 };
 
-// A thread turns 16 codes (one 16-byte load) into 32 bytes of bf16; kGatherIlp
-// of them at once keep enough loads in flight. Bound: bytes (576 read and
-// 1,152 written a row).
-constexpr int kGatherIlp = 4;
+// A thread turns 16 codes (one 16-byte load) into 32 bytes of bf16 (one
+// 32-byte store), eight rows of the same column for eight loads in flight.
+// Bound: bytes (576 read and 1,152 written a row).
+template <int DC, int DR>
+struct GatherCfg {
+  static constexpr int kCols = (DC + DR) / 16;                  // 36 (5)
+  static constexpr int kLanes = DC == 512 ? 8 : 64;             // rows side by side (whole warps)
+  static constexpr int kThr = kCols * kLanes;
+  static constexpr int kDeep = 8;
+  static constexpr int kRows = kLanes * kDeep;
+};
 
 template <int DC, int DR>
-__global__ void __launch_bounds__(kThreads) cache_gather_kernel(const __grid_constant__ GatherArgs a) {
-  constexpr int kRow = (DC + DR) / 16;
-  const int ps = a.cache.page_size;
+__global__ void __launch_bounds__(GatherCfg<DC, DR>::kThr)
+    cache_gather_kernel(const __grid_constant__ GatherArgs a) {
+  using C = GatherCfg<DC, DR>;
+  const int ps = a.cache.page_size, shift = 31 - __clz(ps);
   const int len = __ldg(a.batch.seq_lens + a.seq);
-  const int end = min(a.pos0 + a.n_rows, min(len, a.batch.max_pages * ps));
+  const int end = min(a.pos0 + a.n_rows, min(len, a.batch.max_pages << shift));
   if (blockIdx.x == gridDim.x - 1) {
     unsigned int site = end < a.pos0 + a.n_rows ? kCacheSiteSeq : 0u;
-    for (int j = a.pos0 / ps + static_cast<int>(threadIdx.x); static_cast<int64_t>(j) * ps < end;
-         j += blockDim.x)
+    for (int j = (a.pos0 >> shift) + static_cast<int>(threadIdx.x);
+         (static_cast<int64_t>(j) << shift) < end; j += blockDim.x)
       if (!page_ok(a.cache, page_of(a.batch, a.seq, j))) site = max(site, kCacheSitePage);
     write_status(a.ws, site);
     return;
   }
-  uint4 v[kGatherIlp];
-  float s[kGatherIlp];
-  const int64_t x0 = static_cast<int64_t>(blockIdx.x) * kThreads * kGatherIlp + threadIdx.x;
+  const int u = threadIdx.x % C::kCols;
+  const int row0 = blockIdx.x * C::kRows + threadIdx.x / C::kCols;
+  const bool lat = u < DC / 16;
+  const uint8_t* pool = lat ? a.cache.latent + u * 16 : a.cache.rope + (u - DC / 16) * 16;
+  const int64_t stride = lat ? a.cache.latent_page_stride : a.cache.rope_page_stride;
+  const int width = lat ? DC : DR;
+  int page[C::kDeep];
 #pragma unroll
-  for (int i = 0; i < kGatherIlp; ++i) {
-    const int64_t x = x0 + i * kThreads;
-    const int64_t pos = a.pos0 + x / kRow;
-    const int u = static_cast<int>(x % kRow);
-    s[i] = 0.f;
-    if (pos >= end) continue;
-    const int page = page_of(a.batch, a.seq, pos / ps), row = static_cast<int>(pos % ps);
-    if (!page_ok(a.cache, page)) continue;
-    s[i] = pow2f(scale_exp(__ldg(a.cache.scale + page)));
-    const uint8_t* src = u < DC / 16
-                             ? a.cache.latent + page * a.cache.latent_page_stride + row * DC + u * 16
-                             : a.cache.rope + page * a.cache.rope_page_stride + row * DR +
-                                   (u - DC / 16) * 16;
-    v[i] = __ldg(reinterpret_cast<const uint4*>(src));
+  for (int i = 0; i < C::kDeep; ++i) {
+    const int pos = a.pos0 + row0 + i * C::kLanes;
+    page[i] = pos < end ? page_of(a.batch, a.seq, pos >> shift) : -1;
   }
+  uint4 v[C::kDeep];
+  float s[C::kDeep];
 #pragma unroll
-  for (int i = 0; i < kGatherIlp; ++i) {
-    if (s[i] == 0.f) continue;
-    const int64_t x = x0 + i * kThreads, row = x / kRow;
-    const int u = static_cast<int>(x % kRow);
+  for (int i = 0; i < C::kDeep; ++i) {
+    if (!page_ok(a.cache, page[i])) page[i] = -1;
+    s[i] = 0.f;
+    if (page[i] >= 0) {
+      const int row = (a.pos0 + row0 + i * C::kLanes) & (ps - 1);
+      v[i] = __ldg(reinterpret_cast<const uint4*>(pool + page[i] * stride + row * width));
+      s[i] = __ldg(a.cache.scale + page[i]);
+    }
+  }
+  uint16_t* out = lat ? a.latent + u * 16 : a.rope + (u - DC / 16) * 16;
+#pragma unroll
+  for (int i = 0; i < C::kDeep; ++i) {
+    if (page[i] < 0) continue;
+    const float f = pow2f(scale_exp(s[i]));
     const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
     uint32_t o[8];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float2 lo = e4m3x2_to_f32(w[e]), hi = e4m3x2_to_f32(w[e] >> 16);
-      o[2 * e] = pack_bf16x2(lo.x * s[i], lo.y * s[i]);
-      o[2 * e + 1] = pack_bf16x2(hi.x * s[i], hi.y * s[i]);
+      o[2 * e] = pack_bf16x2(lo.x * f, lo.y * f);
+      o[2 * e + 1] = pack_bf16x2(hi.x * f, hi.y * f);
     }
-    uint4* dst = reinterpret_cast<uint4*>(u < DC / 16 ? a.latent + row * DC + u * 16
-                                                      : a.rope + row * DR + (u - DC / 16) * 16);
-    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    uint16_t* dst = out + static_cast<int64_t>(row0 + i * C::kLanes) * width;
+    if (a.wide)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(o[0]),
+                   "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                   : "memory");
+    else {
+      reinterpret_cast<uint4*>(dst)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      reinterpret_cast<uint4*>(dst)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
   }
+}
+
+template <int DC, int DR>
+void launch_gather_t(const GatherArgs& a, cudaStream_t st) {
+  using C = GatherCfg<DC, DR>;
+  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(a.n_rows) + C::kRows - 1) / C::kRows);
+  cache_gather_kernel<DC, DR><<<grid + 1, C::kThr, 0, st>>>(a);
 }
 
 }  // namespace
@@ -403,12 +477,10 @@ cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t st) {
 cudaError_t launch_cache_gather(const dsa_cache& c, const dsa_batch& b, int seq, int pos0,
                                 int n_rows, uint16_t* latent, uint16_t* rope, WsHeader* ws,
                                 cudaStream_t st) {
-  const GatherArgs a{c, b, latent, rope, seq, pos0, n_rows, ws};
-  const int64_t per = static_cast<int64_t>(kThreads) * kGatherIlp;
-  const int64_t units = static_cast<int64_t>(n_rows) * ((c.d_latent + c.d_rope) / 16);
-  const unsigned grid = static_cast<unsigned>((units + per - 1) / per + 1);
-  if (c.d_latent == 512) cache_gather_kernel<512, 64><<<grid, kThreads, 0, st>>>(a);
-  else cache_gather_kernel<64, 16><<<grid, kThreads, 0, st>>>(a);
+  const bool wide = ((reinterpret_cast<uintptr_t>(latent) | reinterpret_cast<uintptr_t>(rope)) & 31u) == 0;
+  const GatherArgs a{c, b, latent, rope, seq, pos0, n_rows, wide, ws};
+  if (c.d_latent == 512) launch_gather_t<512, 64>(a, st);
+  else launch_gather_t<64, 16>(a, st);
   return cudaGetLastError();
 }
 

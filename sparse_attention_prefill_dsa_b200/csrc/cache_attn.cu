@@ -1179,102 +1179,115 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, 1)
 
 // ------------------------------------------------------------------- combine
 
-constexpr int kCombineThreads = 512;
+constexpr int kCombineThreads = 128;
+constexpr int kCombineBlocks = 16;  // per SM
 
-// Joins the partial results of the items that cross CTAs, one query row at a
-// time: out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c. Four groups of 128
-// threads (four dims a thread) take every fourth part. Also collects the
-// CTAs' status.
+// Joins the partial results of the items that cross CTAs: out = sum_c
+// 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c. A block takes 128 dims of a query
+// row, its four warps every fourth part each (one long sequence is in up to
+// 148 parts); the weights are in lanes. Also collects the CTAs' status.
 template <int R>
 __global__ void __launch_bounds__(kCombineThreads)
     cache_attn_combine(const __grid_constant__ CacheAttnParams p, int n_ctas) {
+  constexpr int kRounds = (kMaxCtas + 31) / 32;
   __shared__ int s_owner[kMaxCtas];
-  __shared__ int s_count;
-  __shared__ float s_w[kMaxCtas + 2];
-  __shared__ float4 s_acc[3][128];
-  const int tid = threadIdx.x;
-  if (tid < 32) {  // the CTAs that end such an item, in order (the same list in every block)
-    int n = 0;
-    for (int c0 = 0; c0 < n_ctas; c0 += 32) {
-      const bool has = c0 + tid < n_ctas && p.meta[c0 + tid].n_rows > 0;
-      const uint32_t b = __ballot_sync(0xffffffffu, has);
-      if (has) s_owner[n + __popc(b & ((1u << tid) - 1u))] = c0 + tid;
-      n += __popc(b);
+  __shared__ uint32_t s_has[kRounds];
+  __shared__ float4 s_acc[3][32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the CTAs that end such an item, in order (the same list in every block)
+  unsigned int status = 0, info = 0;
+  for (int c0 = 32 * warp; c0 < 32 * kRounds; c0 += kCombineThreads) {
+    const int c = c0 + lane;
+    bool has = false;
+    if (c < n_ctas) {
+      has = p.meta[c].n_rows > 0;
+      const unsigned int st = p.meta[c].status;
+      if (st != 0u) {
+        status = st;
+        info = p.meta[c].info;
+      }
     }
-    if (tid == 0) s_count = n;
+    const uint32_t b = __ballot_sync(0xffffffffu, has);
+    if (lane == 0) s_has[c0 >> 5] = b;
   }
+  const int any = __syncthreads_or(status != 0u);
   if (blockIdx.x == 0 && tid == 0) {
-    unsigned int status = 0, info = 0;
-    for (int c = 0; c < n_ctas && status == 0u; ++c) {
-      status = p.meta[c].status;
-      info = p.meta[c].info;
-    }
-    p.a.ws->status_info = info;
-    p.a.ws->status = status;
+    p.a.ws->status = 0u;
+    p.a.ws->status_info = 0u;
+  }
+  int count = 0;
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    const uint32_t b = s_has[i];
+    if (warp == i % 4 && ((b >> lane) & 1u)) s_owner[count + __popc(b & ((1u << lane) - 1u))] = 32 * i + lane;
+    count += __popc(b);
   }
   __syncthreads();
-  const int work = s_count * R;
+  if (blockIdx.x == 0 && any && status != 0u) report(p.a.ws, status, info);
+  const int work = count * R * 4;
   for (int u = blockIdx.x; u < work; u += gridDim.x) {
-    const int c1 = s_owner[u / R], r = u % R;
-    const CtaMeta me = p.meta[c1];
-    if (r >= me.n_rows) continue;
-    const int c0 = me.first, n = c1 - c0 + 1;
-    auto part = [&](int j) { return 2ll * (c0 + j) + (j == 0 ? 1 : 0); };
-    // weights of the parts, in the first warp
-    __syncthreads();
-    if (tid < 32) {
-      float mx = -INFINITY;
-      for (int j = tid; j < n; j += 32) mx = fmaxf(mx, p.part_ml[part(j) * R + r].x);
-      mx = warp_max(mx);
-      float sum = 0.f;
-      for (int j = tid; j < n; j += 32) {
-        const float2 v = p.part_ml[part(j) * R + r];
-        const float w = v.x == -INFINITY ? 0.f : exp2f(v.x - mx);
-        s_w[j] = w;
-        sum += w * v.y;
-      }
+    const int c1 = s_owner[u / (4 * R)], r = (u >> 2) % R, quarter = u & 3;
+    const int row = p.meta[c1].row, c0 = p.meta[c1].first, n = c1 - c0 + 1;
+    if (r >= p.meta[c1].n_rows) continue;
+    // (the item's first part is its CTA's second slot)
+    auto part = [&](int j) { return (2ll * (c0 + j) + (j == 0 ? 1 : 0)) * R + r; };
+    float2 ml[kRounds];
+    float mx = -INFINITY;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (tid == 0) {
-        s_w[kMaxCtas + 1] = sum > 0.f ? 1.f / sum : 0.f;
-        if (p.a.lse)
-          p.a.lse[static_cast<int64_t>(me.row) + r] =
-              sum > 0.f ? (mx + log2f(sum)) * 0.69314718055994531f : -INFINITY;
-      }
+    for (int i = 0; i < kRounds; ++i) {
+      const int j = 32 * i + lane;
+      ml[i] = j < n ? p.part_ml[part(j)] : make_float2(-INFINITY, 0.f);
+      mx = fmaxf(mx, ml[i].x);
     }
-    __syncthreads();
-    const int group = tid >> 7, d4 = tid & 127;
+    mx = warp_max(mx);
+    float sum = 0.f, w[kRounds];
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+      w[i] = ml[i].x == -INFINITY ? 0.f : exp2f(ml[i].x - mx);
+      sum += w[i] * ml[i].y;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
 #pragma unroll 4
-    for (int j = group; j < n; j += 4) {
-      const float w = s_w[j];
-      const float4 v = reinterpret_cast<const float4*>(p.part_o + (part(j) * R + r) * kDC)[d4];
-      if (w > 0.f) {
-        acc.x = fmaf(w, v.x, acc.x);
-        acc.y = fmaf(w, v.y, acc.y);
-        acc.z = fmaf(w, v.z, acc.z);
-        acc.w = fmaf(w, v.w, acc.w);
+      for (int jj = warp; jj < min(n - 32 * i, 32); jj += 4) {
+        const float f = __shfl_sync(0xffffffffu, w[i], jj);
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(
+                                    p.part_o + part(32 * i + jj) * kDC + quarter * 128) + lane);
+        if (f > 0.f) {
+          acc.x = fmaf(f, v.x, acc.x);
+          acc.y = fmaf(f, v.y, acc.y);
+          acc.z = fmaf(f, v.z, acc.z);
+          acc.w = fmaf(f, v.w, acc.w);
+        }
       }
     }
-    if (group > 0) s_acc[group - 1][d4] = acc;
+    if (warp > 0) s_acc[warp - 1][lane] = acc;
     __syncthreads();
-    if (group == 0) {
+    if (warp == 0) {
 #pragma unroll
       for (int j = 0; j < 3; ++j) {
-        const float4 v = s_acc[j][d4];
+        const float4 v = s_acc[j][lane];
         acc.x += v.x;
         acc.y += v.y;
         acc.z += v.z;
         acc.w += v.w;
       }
-      const float inv = s_w[kMaxCtas + 1];
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
       const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
       const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
       uint2 v;
       v.x = *reinterpret_cast<const uint32_t*>(&lo);
       v.y = *reinterpret_cast<const uint32_t*>(&hi);
-      *reinterpret_cast<uint2*>(p.a.out + (static_cast<int64_t>(me.row) + r) * kDC + 4 * d4) = v;
+      *reinterpret_cast<uint2*>(p.a.out + (static_cast<int64_t>(row) + r) * kDC + quarter * 128 +
+                                4 * lane) = v;
+      if (lane == 0 && quarter == 0 && p.a.lse)
+        p.a.lse[static_cast<int64_t>(row) + r] =
+            sum > 0.f ? (mx + log2f(sum)) * 0.69314718055994531f : -INFINITY;
     }
+    __syncthreads();  // before s_acc is written again
   }
 }
 
@@ -1429,7 +1442,7 @@ cudaError_t launch_tc(const CacheAttnArgs& a, void* scratch, cudaStream_t st) {
   cache_attn_tc<R><<<grid, Cfg<R>::kThreads, Cfg<R>::kSmemBytes, st>>>(p, ml, mr);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  cache_attn_combine<R><<<grid, kCombineThreads, 0, st>>>(p, grid);
+  cache_attn_combine<R><<<grid * kCombineBlocks, kCombineThreads, 0, st>>>(p, grid);
   return cudaGetLastError();
 }
 
