@@ -155,17 +155,23 @@ struct SegmentWalk {
   int k0, k1;
   int64_t left;  // tiles after this segment
   int64_t slots;
-  // From the item of `slot`, tile k, for n > 0 tiles.
-  __device__ void begin(const CacheAttnArgs& a, int64_t slot, int k, int64_t n) {
-    slots = slots_of<R>(a);
-    w.seek(a, slot);
-    w.item(a, it);
-    k0 = k;
-    k1 = static_cast<int>(min(static_cast<int64_t>(it.nt), k + n));
+  bool at_first = true;  // the walk has not been set up yet
+  int64_t slot0;
+  // From the CTA's first segment, of the item of `slot`, for n > 0 tiles.
+  __device__ void begin(const Segment& first, int64_t slot, int64_t n) {
+    it = first.it;
+    k0 = first.k0;
+    k1 = first.k1;
     left = n - (k1 - k0);
+    slot0 = slot;
   }
   __device__ bool next(const CacheAttnArgs& a) {
     if (left <= 0) return false;
+    if (at_first) {
+      slots = slots_of<R>(a);
+      w.seek(a, slot0);
+      at_first = false;
+    }
     do {
       w.next(a);
       if (w.slot >= slots) return false;
@@ -199,8 +205,7 @@ struct Misc {
   unsigned int status, info;  // stands in for the header of a workspace in report()
   uint32_t tmem;
   int abort_flag;
-  long long slot, n_tiles, total;
-  int k0;
+  long long slot, n_tiles, total, begin;
 };
 static_assert(sizeof(Misc) <= 48, "misc");
 
@@ -242,6 +247,7 @@ struct Cfg {
   static constexpr int kThreads = 32 * (kWarps + 3);  // + producer, MMA, relay
   static constexpr int kSync = 32 * (kWarps + 1);     // the softmax warps and one other
   static constexpr bool kSplitO = R == 32;         // hi and lo of P onto their own columns of O
+  static constexpr bool kLockstep = R == 32;       // PV of a tile before QK^T of the next
   static constexpr int kQChunk = 2 * R * 128;      // 128 dims of the hi and lo rows
   static constexpr int kQBytes = 2 * R * (kDC + kDR);
   static constexpr int kTmemS = 0, kTmemO = 4 * R;  // S^T [2 buffers][2R], O^T [4][64]
@@ -330,6 +336,7 @@ __device__ __forceinline__ float warp_transpose_sum(float (&v)[16]) {
 __device__ __noinline__ long long part_begin(long long total, int grid, int c) {
   const unsigned long long g = min(static_cast<long long>(grid), total);
   if (static_cast<unsigned long long>(c) >= g) return total;
+  if (total < (1 << 24)) return static_cast<unsigned>(total) * c / static_cast<unsigned>(g);
   return static_cast<long long>(static_cast<unsigned long long>(total) * c / g);
 }
 
@@ -344,10 +351,10 @@ __device__ __noinline__ int cta_of_tile(long long at, long long total, int grid,
   return lo;
 }
 
-// Counts the tiles of all items and finds this CTA's part. All threads;
-// `scan` is scratch for a long long of each warp.
+// Counts the tiles of all items and finds this CTA's part and its first
+// segment. All threads; `scan` is scratch for a long long of each warp.
 template <int R>
-__device__ void schedule(const CacheAttnArgs& a, Misc* ms, long long* scan) {
+__device__ void schedule(const CacheAttnArgs& a, Misc* ms, long long* scan, Segment* first) {
   constexpr int kThreads = Cfg<R>::kThreads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // the slots need cu_seqlens that ascend; if they do not, there is no work
@@ -388,20 +395,27 @@ __device__ void schedule(const CacheAttnArgs& a, Misc* ms, long long* scan) {
   const long long begin = part_begin(total, gridDim.x, blockIdx.x);
   const long long end = part_begin(total, gridDim.x, blockIdx.x + 1);
   const long long lo = before + inc - sum;
-  if (begin < end && lo <= begin && begin < lo + sum) {  // one thread
+  if (begin < end && lo <= begin && begin < lo + sum) {
+    // this thread's: it publishes the CTA's first segment
     long long at = lo;
-    w.seek(a, s0);
-    int n;
-    while (at + (n = w.item(a, it)) <= begin) {
-      at += n;
-      w.next(a);
+    int n = static_cast<int>(sum);
+    if (s1 - s0 > 1) {
+      w.seek(a, s0);
+      while (at + (n = w.item(a, it)) <= begin) {
+        at += n;
+        w.next(a);
+      }
     }
-    ms->slot = w.slot;
-    ms->k0 = static_cast<int>(begin - at);
+    first->it = it;
+    first->k0 = static_cast<int>(begin - at);
+    first->k1 = static_cast<int>(min(static_cast<long long>(it.nt), first->k0 + end - begin));
+    first->more = first->k1 - first->k0 < end - begin;
+    ms->slot = s0 + (s1 - s0 > 1 ? w.slot - s0 : 0);
   }
   if (tid == 0) {
     ms->n_tiles = end - begin;
     ms->total = total;
+    ms->begin = begin;
   }
   __syncthreads();
 }
@@ -561,15 +575,19 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
 }
 
 // The order of a CTA's matrix products, as the MMA warp issues them and the
-// relay warp sees them done: QK^T runs one tile ahead of PV, but a segment's
+// relay warp sees them done. At R = 64 QK^T runs one tile ahead of PV, so that
+// the softmax of one tile overlaps the products of another; but a segment's
 // first QK^T comes after the last PV of the segment before (whose epilogue
-// then overlaps it).
+// then overlaps it). At R = 32 the bytes bound: PV follows its QK^T at once and
+// does not wait for the next tile to land, so that a tile's place is loaded
+// again while the other's is still on its way.
 template <int R>
 struct Order {
+  static constexpr int kAhead = Cfg<R>::kLockstep ? 1 : 2;
   int q = 0, v = 0;      // next tiles of QK^T and PV
   int seg = 0, left = 0; // segment of tile q, its tiles from q on (0: not looked at yet)
   int n;
-  __device__ __forceinline__ bool pv_next() const { return q - v == 2 || (v < q && (q == n || left == 0)); }
+  __device__ __forceinline__ bool pv_next() const { return q - v == kAhead || (v < q && (q == n || left == 0)); }
   // Before QK^T of tile q: looks up its segment if it begins one.
   __device__ __forceinline__ bool begin_q(const Ctx<R>& x, bool& ok) {
     if (left > 0) return false;
@@ -591,8 +609,8 @@ __device__ void producer(const Ctx<R>& x, const CUtensorMap* ml, const CUtensorM
   const int lane = threadIdx.x & 31, ps = a.cache.page_size, npt = kKeys / ps;
   const int n = static_cast<int>(x.ms()->n_tiles);
   SegmentWalk<R> sg;
-  sg.begin(a, x.ms()->slot, x.ms()->k0, x.ms()->n_tiles);
-  int seg = 0;
+  sg.begin(*x.segment(0), x.ms()->slot, n);
+  int seg = 1;
   auto publish = [&] {
     if (lane == 0) {
       Segment* out = x.segment(seg);
@@ -604,8 +622,8 @@ __device__ void producer(const Ctx<R>& x, const CUtensorMap* ml, const CUtensorM
     }
     ++seg;
   };
-  publish();
   if (lane == 0) {
+    mbar_arrive(x.bar(kSeg));  // (the first is there)
     // an item that began in another CTA and ends here: this CTA's entry tells
     // the combine pass of it
     CtaMeta& me = x.p.meta[blockIdx.x];
@@ -613,8 +631,7 @@ __device__ void producer(const Ctx<R>& x, const CUtensorMap* ml, const CUtensorM
     if (sg.k0 > 0 && sg.k1 == sg.it.nt) {
       me.row = sg.it.row;
       me.n_rows = sg.it.n_rows;
-      me.first = cta_of_tile(part_begin(x.ms()->total, gridDim.x, blockIdx.x) - sg.k0,
-                             x.ms()->total, gridDim.x, blockIdx.x);
+      me.first = cta_of_tile(x.ms()->begin - sg.k0, x.ms()->total, gridDim.x, blockIdx.x);
     }
   }
   // The next tile to plan is tile k of the segment. Its plan: this lane's page
@@ -976,6 +993,7 @@ __device__ void softmax_warps(const Ctx<R>& x) {
     }
 #pragma unroll 1
     for (int k = 0; k < n_seg; ++k, ++i) {
+      if (C::kLockstep && k > 0) named_sync(kPvReady, C::kSync);
       if (i > 0) named_sync(kSReady + (i & 1), C::kSync);
       tc_fence_after();
       const int e_key = e_page == kNoPage ? 0 : e_page;
@@ -1021,7 +1039,8 @@ __device__ void softmax_warps(const Ctx<R>& x) {
       float over = y[0];
 #pragma unroll
       for (int r = 1; r < HR; ++r) over = fmaxf(over, y[r]);
-      bool pv_due = k > 0;  // the previous PV has to be waited for (a segment's last one was)
+      // the previous PV has to be waited for (a segment's last one was)
+      bool pv_due = !C::kLockstep && k > 0;
       if (named_or(kVote + g, 128, over > 8.f) || unset != 0u) {
         // a new reference for the rows that need one
         float mx = -INFINITY;
@@ -1054,7 +1073,7 @@ __device__ void softmax_warps(const Ctx<R>& x) {
             fr[r] = __shfl_sync(0xffffffffu, f, r);
             l[r] *= fr[r];
           }
-          if (pv_due) {
+          if (k > 0) {
 #pragma unroll 1
             for (int c = 0; c < (C::kSplitO ? 8 : 4); ++c) {
               const uint32_t col = lanes + C::kTmemO + (C::kSplitO ? 32 : 64) * c + g * HR;
@@ -1148,7 +1167,7 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, 1)
   }
   if (warp == C::kWarps + 1) tmem_alloc(&ms->tmem, 512);
   __syncthreads();  // the status word before schedule() may report
-  schedule<R>(p.a, ms, reinterpret_cast<long long*>(x.s() + C::kOffM));  // ends with a barrier
+  schedule<R>(p.a, ms, reinterpret_cast<long long*>(x.s() + C::kOffM), x.segment(0));  // ends with a barrier
   tc_fence_after();
   // All 512 columns are this CTA's, so they begin at 0; operands are at
   // constant addresses on that account.
@@ -1180,112 +1199,167 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, 1)
 // ------------------------------------------------------------------- combine
 
 constexpr int kCombineThreads = 128;
-constexpr int kCombineBlocks = 16;  // per SM
+constexpr int kCombineBlocks = 8;  // per SM
+
+// Parts of an item up to which a warp joins a whole row by itself.
+constexpr int kFewParts = 4;
+
+// The weights 2^(m_j - M) of one query row's parts (lane j of a warp, or
+// s_w[j] where there are more than 32) and the sum of the weighted l.
+struct RowParts {
+  float w, mx, sum;
+  template <class Part>
+  __device__ __forceinline__ void load(const float2* part_ml, int n, float* s_w, Part part) {
+    const int lane = threadIdx.x & 31;
+    mx = -INFINITY;
+#pragma unroll 1
+    for (int j = lane; j < n; j += 32) mx = fmaxf(mx, __ldcg(part_ml + part(j)).x);
+    mx = warp_max(mx);
+    w = sum = 0.f;
+#pragma unroll 1
+    for (int j = lane; j < n; j += 32) {
+      const float2 ml = __ldcg(part_ml + part(j));
+      w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - mx);
+      sum += w * ml.y;
+      if (s_w) s_w[j] = w;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  }
+  __device__ __forceinline__ float inv() const { return sum > 0.f ? 1.f / sum : 0.f; }
+  __device__ __forceinline__ float lse() const {
+    return sum > 0.f ? (mx + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+  }
+};
+
+__device__ __forceinline__ void add_part(float4& acc, float f, const float4& v) {
+  // (O of a part without keys is 0: its p were)
+  acc.x = fmaf(f, v.x, acc.x);
+  acc.y = fmaf(f, v.y, acc.y);
+  acc.z = fmaf(f, v.z, acc.z);
+  acc.w = fmaf(f, v.w, acc.w);
+}
+
+__device__ __forceinline__ void store_bf16x4(uint16_t* dst, const float4& v, float f) {
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * f, v.y * f);
+  const __nv_bfloat162 hi = __floats2bfloat162_rn(v.z * f, v.w * f);
+  *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                              *reinterpret_cast<const uint32_t*>(&hi));
+}
 
 // Joins the partial results of the items that cross CTAs: out = sum_c
-// 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c. A block takes 128 dims of a query
-// row, its four warps every fourth part each (one long sequence is in up to
-// 148 parts); the weights are in lanes. Also collects the CTAs' status.
+// 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c. An item in few parts (a batch: most
+// are in two) takes a warp for each row; one in many (a long sequence is in up
+// to 148) a block for 128 dims of a row, its warps every fourth part each.
+// Also collects the CTAs' status.
 template <int R>
 __global__ void __launch_bounds__(kCombineThreads)
     cache_attn_combine(const __grid_constant__ CacheAttnParams p, int n_ctas) {
   constexpr int kRounds = (kMaxCtas + 31) / 32;
-  __shared__ int s_owner[kMaxCtas];
-  __shared__ uint32_t s_has[kRounds];
+  __shared__ float s_w[4][kMaxCtas];  // a warp's own copy
+  __shared__ int4 s_few[kMaxCtas], s_many[kMaxCtas];  // last CTA, first CTA, row, rows
+  __shared__ uint32_t s_has[2][kRounds];
   __shared__ float4 s_acc[3][32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // the CTAs that end such an item, in order (the same list in every block)
+  // the CTAs that end such an item, in order (the same lists in every block)
   unsigned int status = 0, info = 0;
-  for (int c0 = 32 * warp; c0 < 32 * kRounds; c0 += kCombineThreads) {
-    const int c = c0 + lane;
-    bool has = false;
-    if (c < n_ctas) {
-      has = p.meta[c].n_rows > 0;
-      const unsigned int st = p.meta[c].status;
-      if (st != 0u) {
-        status = st;
-        info = p.meta[c].info;
+  int4 mine[(kRounds + 3) / 4];
+  int kind[(kRounds + 3) / 4];
+#pragma unroll
+  for (int k = 0; k < (kRounds + 3) / 4; ++k) {
+    const int i = warp + 4 * k, c = 32 * i + lane;
+    kind[k] = -1;
+    if (i < kRounds && c < n_ctas) {
+      const CtaMeta me = p.meta[c];
+      mine[k] = make_int4(c, me.first, me.row, me.n_rows);
+      if (me.n_rows > 0) kind[k] = c - me.first + 1 > kFewParts ? 1 : 0;
+      if (me.status != 0u) {
+        status = me.status;
+        info = me.info;
       }
     }
-    const uint32_t b = __ballot_sync(0xffffffffu, has);
-    if (lane == 0) s_has[c0 >> 5] = b;
+    const uint32_t few = __ballot_sync(0xffffffffu, kind[k] == 0);
+    const uint32_t many = __ballot_sync(0xffffffffu, kind[k] == 1);
+    if (lane == 0 && i < kRounds) {
+      s_has[0][i] = few;
+      s_has[1][i] = many;
+    }
   }
-  const int any = __syncthreads_or(status != 0u);
   if (blockIdx.x == 0 && tid == 0) {
     p.a.ws->status = 0u;
     p.a.ws->status_info = 0u;
   }
-  int count = 0;
+  __syncthreads();
+  int n_few = 0, n_many = 0;
 #pragma unroll
   for (int i = 0; i < kRounds; ++i) {
-    const uint32_t b = s_has[i];
-    if (warp == i % 4 && ((b >> lane) & 1u)) s_owner[count + __popc(b & ((1u << lane) - 1u))] = 32 * i + lane;
-    count += __popc(b);
+    const uint32_t few = s_has[0][i], many = s_has[1][i], below = (1u << lane) - 1u;
+    if (warp == i % 4) {
+      if (kind[i / 4] == 0) s_few[n_few + __popc(few & below)] = mine[i / 4];
+      if (kind[i / 4] == 1) s_many[n_many + __popc(many & below)] = mine[i / 4];
+    }
+    n_few += __popc(few);
+    n_many += __popc(many);
   }
   __syncthreads();
-  if (blockIdx.x == 0 && any && status != 0u) report(p.a.ws, status, info);
-  const int work = count * R * 4;
-  for (int u = blockIdx.x; u < work; u += gridDim.x) {
-    const int c1 = s_owner[u / (4 * R)], r = (u >> 2) % R, quarter = u & 3;
-    const int row = p.meta[c1].row, c0 = p.meta[c1].first, n = c1 - c0 + 1;
-    if (r >= p.meta[c1].n_rows) continue;
+  if (blockIdx.x == 0 && status != 0u) report(p.a.ws, status, info);
+  for (int u = blockIdx.x * 4 + warp; u < n_few * R; u += gridDim.x * 4) {
+    const int4 me = s_few[u / R];
+    const int r = u % R, c0 = me.y, n = me.x - c0 + 1;
+    if (r >= me.w) continue;
     // (the item's first part is its CTA's second slot)
     auto part = [&](int j) { return (2ll * (c0 + j) + (j == 0 ? 1 : 0)) * R + r; };
-    float2 ml[kRounds];
-    float mx = -INFINITY;
+    float4 v[kFewParts][4];
 #pragma unroll
-    for (int i = 0; i < kRounds; ++i) {
-      const int j = 32 * i + lane;
-      ml[i] = j < n ? p.part_ml[part(j)] : make_float2(-INFINITY, 0.f);
-      mx = fmaxf(mx, ml[i].x);
-    }
-    mx = warp_max(mx);
-    float sum = 0.f, w[kRounds];
+    for (int j = 0; j < kFewParts; ++j)
+      if (j < n) {
+        const float4* src = reinterpret_cast<const float4*>(p.part_o + part(j) * kDC);
 #pragma unroll
-    for (int i = 0; i < kRounds; ++i) {
-      w[i] = ml[i].x == -INFINITY ? 0.f : exp2f(ml[i].x - mx);
-      sum += w[i] * ml[i].y;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < kRounds; ++i) {
-#pragma unroll 4
-      for (int jj = warp; jj < min(n - 32 * i, 32); jj += 4) {
-        const float f = __shfl_sync(0xffffffffu, w[i], jj);
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(
-                                    p.part_o + part(32 * i + jj) * kDC + quarter * 128) + lane);
-        if (f > 0.f) {
-          acc.x = fmaf(f, v.x, acc.x);
-          acc.y = fmaf(f, v.y, acc.y);
-          acc.z = fmaf(f, v.z, acc.z);
-          acc.w = fmaf(f, v.w, acc.w);
-        }
+        for (int e = 0; e < 4; ++e) v[j][e] = __ldcg(src + 32 * e + lane);
       }
+    RowParts rp;
+    rp.load(p.part_ml, n, nullptr, part);
+    const int64_t row = static_cast<int64_t>(me.z) + r;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < kFewParts; ++j) {
+        const float f = __shfl_sync(0xffffffffu, rp.w, j);
+        if (j < n) add_part(acc, f, v[j][e]);
+      }
+      store_bf16x4(p.a.out + row * kDC + 128 * e + 4 * lane, acc, rp.inv());
+    }
+    if (lane == 0 && p.a.lse) p.a.lse[row] = rp.lse();
+  }
+  for (int u = blockIdx.x; u < n_many * R * 4; u += gridDim.x) {
+    const int4 me = s_many[u / (4 * R)];
+    const int r = (u >> 2) % R, quarter = u & 3, c0 = me.y, n = me.x - c0 + 1;
+    if (r >= me.w) continue;
+    auto part = [&](int j) { return (2ll * (c0 + j) + (j == 0 ? 1 : 0)) * R + r; };
+    RowParts rp;
+    rp.load(p.part_ml, n, s_w[warp], part);
+    __syncwarp();
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int j0 = warp; j0 < n; j0 += 32) {
+      float4 v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        v[k] = j0 + 4 * k < n ? __ldcg(reinterpret_cast<const float4*>(
+                                           p.part_o + part(j0 + 4 * k) * kDC + quarter * 128) + lane)
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) add_part(acc, j0 + 4 * k < n ? s_w[warp][j0 + 4 * k] : 0.f, v[k]);
     }
     if (warp > 0) s_acc[warp - 1][lane] = acc;
     __syncthreads();
     if (warp == 0) {
 #pragma unroll
-      for (int j = 0; j < 3; ++j) {
-        const float4 v = s_acc[j][lane];
-        acc.x += v.x;
-        acc.y += v.y;
-        acc.z += v.z;
-        acc.w += v.w;
-      }
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
-      const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-      const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-      uint2 v;
-      v.x = *reinterpret_cast<const uint32_t*>(&lo);
-      v.y = *reinterpret_cast<const uint32_t*>(&hi);
-      *reinterpret_cast<uint2*>(p.a.out + (static_cast<int64_t>(row) + r) * kDC + quarter * 128 +
-                                4 * lane) = v;
-      if (lane == 0 && quarter == 0 && p.a.lse)
-        p.a.lse[static_cast<int64_t>(row) + r] =
-            sum > 0.f ? (mx + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+      for (int j = 0; j < 3; ++j) add_part(acc, 1.f, s_acc[j][lane]);
+      const int64_t row = static_cast<int64_t>(me.z) + r;
+      store_bf16x4(p.a.out + row * kDC + quarter * 128 + 4 * lane, acc, rp.inv());
+      if (lane == 0 && quarter == 0 && p.a.lse) p.a.lse[row] = rp.lse();
     }
     __syncthreads();  // before s_acc is written again
   }
