@@ -217,6 +217,7 @@ enum Bars {
   kPvDone = 22,           // PV of a tile is done
   kQFull,                 // the segment's Q is written
   kOFree,                 // the segment's O has been read
+  kPFull,                 // P of a tile is written (kPollP)
   kSeg,                   // [kSegSlots] a segment is published
   kInfo = kSeg + kSegSlots,  // [4] a tile's info is in place
   kDrain = kInfo + 4,
@@ -226,28 +227,28 @@ enum Bars {
 // Hardware barriers. The MMAs read their operands from shared memory at its
 // full 128 bytes a clock, and whatever else reads it then waits for a gap
 // between two of them (a dependent load takes 114 clocks instead of 40, and
-// warps that poll an mbarrier wait for each other). So per tile one relay warp
-// polls for all softmax warps, and the rest of the exchange between them and
-// the MMA warp is on these, which take no shared memory.
+// warps that poll an mbarrier wait for each other). So two relay warps poll for
+// all softmax warps, and the rest of the exchange between them and the MMA warp
+// is on these, which take no shared memory. Those in pairs go by the tile's
+// parity: one side may be a tile ahead of the other, never two (a tile's place
+// in shared memory is loaded again only after its PV).
 enum HwBars {
-  kVote = 1,    // [groups] within a softmax warpgroup
-  kAll = 5,     // all softmax warps
-  kSReady = 6,   // [2] relay -> softmax: S of a tile, and the info of the next. Two of
-                 // them, by the tile's parity: QK^T of two tiles can be done before
-                 // the softmax takes note of the first
-  kPvReady = 8,  // relay, softmax: PV of a tile is done
-  kSFree = 9,    // [2] softmax -> MMA: S has been read
-  kPReady = 11   // softmax -> MMA: P is written
+  kVote = 1,     // [groups] within a softmax warpgroup
+  kAll = 5,      // all softmax warps
+  kSReady = 6,   // [2] relay -> softmax: S of a tile, and the info of the next
+  kPvReady = 8,  // [2] relay -> softmax: PV of a tile is done
+  kSFree = 10,   // [2] softmax -> MMA: S has been read
+  kPReady = 12   // softmax -> MMA: P is written (not kPollP)
 };
 
 template <int R>
 struct Cfg {
   static constexpr int kGroups = R / HR;           // softmax warpgroups: warps 0 .. 4 kGroups - 1
   static constexpr int kWarps = 4 * kGroups;       // (a warp reads the TMEM lanes of its index mod 4)
-  static constexpr int kThreads = 32 * (kWarps + 3);  // + producer, MMA, relay
+  static constexpr int kThreads = 32 * (kWarps + 4);  // + producer, MMA, two relays
   static constexpr int kSync = 32 * (kWarps + 1);     // the softmax warps and one other
   static constexpr bool kSplitO = R == 32;         // hi and lo of P onto their own columns of O
-  static constexpr bool kLockstep = R == 32;       // PV of a tile before QK^T of the next
+  static constexpr bool kPollP = R == 32;          // the MMA warp takes what is ready first (below)
   static constexpr int kQChunk = 2 * R * 128;      // 128 dims of the hi and lo rows
   static constexpr int kQBytes = 2 * R * (kDC + kDR);
   static constexpr int kTmemS = 0, kTmemO = 4 * R;  // S^T [2 buffers][2R], O^T [4][64]
@@ -270,7 +271,7 @@ struct Cfg {
   static_assert(kTmemO + 256 <= 512, "tensor memory");
 };
 
-enum Sites { kSiteEmpty = 40, kSiteFull, kSiteSFull, kSitePv, kSiteQ, kSiteO, kSiteSeg, kSiteInfo };
+enum Sites { kSiteEmpty = 40, kSiteFull, kSiteSFull, kSitePv, kSiteQ, kSiteO, kSiteSeg, kSiteInfo, kSiteP };
 
 constexpr int kNoPage = 1 << 20;
 
@@ -574,34 +575,6 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
     if (clock64() - t0 > kWaitLimitCycles) break;
 }
 
-// The order of a CTA's matrix products, as the MMA warp issues them and the
-// relay warp sees them done. At R = 64 QK^T runs one tile ahead of PV, so that
-// the softmax of one tile overlaps the products of another; but a segment's
-// first QK^T comes after the last PV of the segment before (whose epilogue
-// then overlaps it). At R = 32 the bytes bound: PV follows its QK^T at once and
-// does not wait for the next tile to land, so that a tile's place is loaded
-// again while the other's is still on its way.
-template <int R>
-struct Order {
-  static constexpr int kAhead = Cfg<R>::kLockstep ? 1 : 2;
-  int q = 0, v = 0;      // next tiles of QK^T and PV
-  int seg = 0, left = 0; // segment of tile q, its tiles from q on (0: not looked at yet)
-  int n;
-  __device__ __forceinline__ bool pv_next() const { return q - v == kAhead || (v < q && (q == n || left == 0)); }
-  // Before QK^T of tile q: looks up its segment if it begins one.
-  __device__ __forceinline__ bool begin_q(const Ctx<R>& x, bool& ok) {
-    if (left > 0) return false;
-    ok = ok && x.wait_segment(seg);
-    ok = __all_sync(0xffffffffu, ok);
-    left = ok ? x.segment(seg)->k1 - x.segment(seg)->k0 : n - q;
-    return true;
-  }
-  __device__ __forceinline__ void end_q() {
-    ++q;
-    if (--left == 0) ++seg;
-  }
-};
-
 // Producer warp: lane l < 128 / page_size loads the tile's l-th page.
 template <int R>
 __device__ void producer(const Ctx<R>& x, const CUtensorMap* ml, const CUtensorMap* mr) {
@@ -710,8 +683,36 @@ __device__ void producer(const Ctx<R>& x, const CUtensorMap* ml, const CUtensorM
   }
 }
 
-// MMA warp: one thread issues. After a timeout it goes on through the
-// hardware barriers without issuing.
+// Waits until one of two phases is complete: 1 or 2 (the first if both are), 0
+// after a timeout. The whole warp, one answer.
+__device__ __noinline__ int wait_either(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, Misc* ms,
+                                        unsigned site) {
+  const long long t0 = clock64();
+  for (uint32_t i = 1;; ++i) {
+    int r = mbar_test_wait(a, pa) ? 1 : mbar_test_wait(b, pb) ? 2 : 0;
+    if (r == 0 && (i & 63u) == 0u) {
+      if (*reinterpret_cast<volatile int*>(&ms->abort_flag)) r = 3;
+      else if (clock64() - t0 > kWaitLimitCycles) {
+        ms->abort_flag = 1;
+        report(reinterpret_cast<WsHeader*>(&ms->status), kDevTimeout, site);
+        r = 3;
+      }
+    }
+    r = __shfl_sync(0xffffffffu, r, 0);
+    if (r != 0) return r == 3 ? 0 : r;
+  }
+}
+
+// MMA warp: one thread issues. A tile's products are QK^T and, once the softmax
+// has turned S into P, PV; at R = 64 QK^T runs a tile ahead, so that the
+// softmax of one tile overlaps the products of another. At R = 32 the bytes
+// bound, and the warp takes whichever comes first, the next tile's landing or
+// P: a PV that waits for the tile would hold back the place that it frees, and
+// with it the load of the tile after, and a QK^T that waits for P would leave
+// the softmax without work. A segment's first QK^T comes after the last PV of
+// the one before, whose epilogue it overlaps.
+// After a timeout the warp goes on through the hardware barriers without
+// issuing.
 template <int R>
 __device__ void mma_issuer(const Ctx<R>& x) {
   using C = Cfg<R>;
@@ -723,18 +724,27 @@ __device__ void mma_issuer(const Ctx<R>& x) {
   const uint64_t dv = smem_desc(sb + C::kOffStage, 16384, 1024, 2);
   const uint64_t dp = smem_desc(sb + C::kOffP, 512, 512, 4);
   const uint64_t dph = smem_desc(sb + C::kOffStage + kRopeOff, 512, 512, 4);
-  Order<R> o;
-  o.n = __shfl_sync(0xffffffffu, static_cast<int>(x.ms()->n_tiles), 0);
+  const int n = __shfl_sync(0xffffffffu, static_cast<int>(x.ms()->n_tiles), 0);
   const bool lead = elect_one();
   bool ok = true;
-  uint32_t first = 0;  // bit i & 1: tile i is its segment's first
-  int v_seg = -1;      // segment of the last PV
+  int q = 0, v = 0;         // next tiles of QK^T and PV
+  int seg = 0, left = 0;    // segment of tile q, its tiles from q on (0: not looked at yet)
+  uint32_t first = 0;       // bit i & 1: tile i is its segment's first
+  int v_seg = -1;           // segment of the last PV
 #pragma unroll 1
   for (;;) {
-    if (o.pv_next()) {
-      const int i = o.v;
+    bool pv = v < q && (q == n || q - v == 2 || left == 0);
+    if (C::kPollP && !pv && v < q) {
+      const int r = ok ? wait_either(x.bar(kFull + 5 * (q & 1) + 4), (q >> 1) & 1, x.bar(kPFull),
+                                     v & 1, x.ms(), kSiteP) : 0;
+      ok = ok && r != 0;
+      pv = r == 2;
+    }
+    if (pv) {
+      const int i = v;
       const bool fresh = (first >> (i & 1)) & 1u;
-      named_sync(kPReady, C::kSync);
+      if constexpr (C::kPollP) ok = ok && x.wait(kPFull, i & 1, kSiteP);
+      else named_sync(kPReady, C::kSync);
       if (fresh && ++v_seg > 0) ok = ok && x.wait(kOFree, (v_seg - 1) & 1, kSiteO);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
@@ -748,7 +758,7 @@ __device__ void mma_issuer(const Ctx<R>& x) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             mma_f8_ss(d, av + ((kk * 4096) >> 4), bh + ((kk * 2048) >> 4), C::kIdescPV,
-                           kk > 0 ? 1u : fresh ? 0u : 1u);
+                      kk > 0 ? 1u : fresh ? 0u : 1u);
           if constexpr (!C::kSplitO) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
@@ -760,11 +770,16 @@ __device__ void mma_issuer(const Ctx<R>& x) {
         mma_commit(x.bar(kPvDone));
       }
       __syncwarp();
-      if (++o.v == o.n) break;
+      if (++v == n) break;
     } else {
-      const int i = o.q, seg = o.seg;
-      const bool begins = o.begin_q(x, ok);
-      if (begins) ok = ok && x.wait(kQFull, seg & 1, kSiteQ);
+      const int i = q;
+      const bool begins = left == 0;
+      if (begins) {
+        ok = ok && x.wait_segment(seg);
+        ok = __all_sync(0xffffffffu, ok);
+        left = ok ? x.segment(seg)->k1 - x.segment(seg)->k0 : n - q;
+        ok = ok && x.wait(kQFull, seg & 1, kSiteQ);
+      }
       first = (first & ~(1u << (i & 1))) | (begins ? 1u : 0u) << (i & 1);
       if (i >= 2) named_sync(kSFree + (i & 1), C::kSync);
       const uint64_t so = static_cast<uint64_t>((i & 1) * kStageBytes) >> 4;
@@ -778,7 +793,7 @@ __device__ void mma_issuer(const Ctx<R>& x) {
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
             mma_f8_ss(d, dk + so + ((c * kChunkBytes + ks * 32) >> 4),
-                           dq + ((c * C::kQChunk + ks * 32) >> 4), C::kIdescQK, c > 0 || ks > 0);
+                      dq + ((c * C::kQChunk + ks * 32) >> 4), C::kIdescQK, c > 0 || ks > 0);
         }
       }
       ok = ok && x.wait(kFull + 5 * (i & 1) + 4, (i >> 1) & 1, kSiteFull);
@@ -791,7 +806,8 @@ __device__ void mma_issuer(const Ctx<R>& x) {
         mma_commit(x.bar(kSFull + (i & 1)));
       }
       __syncwarp();
-      o.end_q();
+      ++q;
+      if (--left == 0) ++seg;
     }
   }
   // every MMA has to be done before the tensor memory is released
@@ -800,33 +816,22 @@ __device__ void mma_issuer(const Ctx<R>& x) {
   drain_wait(x.bar(kDrain), 0);
 }
 
-// Relay warp: sees the products done, in their order, and tells the softmax
-// warps. It tells them after a timeout, too (they never wait for anything else).
+// Relay warps: one sees S of every tile done, the other PV, and they tell the
+// softmax warps; after a timeout, too.
 template <int R>
-__device__ void relay(const Ctx<R>& x) {
-  using C = Cfg<R>;
-  Order<R> o;
-  o.n = static_cast<int>(x.ms()->n_tiles);
+__device__ void relay(const Ctx<R>& x, bool pv) {
+  const int n = static_cast<int>(x.ms()->n_tiles);
   bool ok = true;
 #pragma unroll 1
-  for (;;) {
-    if (o.pv_next()) {
-      ok = ok && x.wait(kPvDone, o.v & 1, kSitePv);
-      __syncwarp();
-      // (with the softmax warps, not ahead of them: they have then taken note
-      // of the last S but one announced, whose barrier is the next one's)
-      named_sync(kPvReady, C::kSync);
-      if (++o.v == o.n) break;
+  for (int i = 0; i < n; ++i) {
+    if (pv) {
+      ok = ok && x.wait(kPvDone, i & 1, kSitePv);
     } else {
-      const int i = o.q;
-      o.begin_q(x, ok);
       if (i == 0) ok = ok && x.wait(kInfo, 0, kSiteInfo);
-      if (i + 1 < o.n) ok = ok && x.wait(kInfo + ((i + 1) & 3), ((i + 1) >> 2) & 1, kSiteInfo);
+      if (i + 1 < n) ok = ok && x.wait(kInfo + ((i + 1) & 3), ((i + 1) >> 2) & 1, kSiteInfo);
       ok = ok && x.wait(kSFull + (i & 1), (i >> 1) & 1, kSiteSFull);
-      __syncwarp();
-      named_arrive(kSReady + (i & 1), C::kSync);
-      o.end_q();
     }
+    named_arrive((pv ? kPvReady : kSReady) + (i & 1), Cfg<R>::kSync);
   }
 }
 
@@ -856,9 +861,9 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 // rows each: twice the warps to hide the latencies of a tile's chain (load,
 // vote, exp2, conversions), in as many registers. The rows' references and
 // factors are in lanes and come by shuffles, not from shared memory.
-// These warps wait for nothing but the hardware barriers, which the relay and
-// the MMA warp always reach, in any order of theirs: after a timeout all go
-// through the barriers of every tile, and nothing is stored.
+// These warps wait for nothing but the hardware barriers, which the relays
+// always reach: after a timeout all go through the barriers of every tile, and
+// nothing is stored.
 template <int R>
 __device__ void softmax_warps(const Ctx<R>& x) {
   using C = Cfg<R>;
@@ -896,7 +901,7 @@ __device__ void softmax_warps(const Ctx<R>& x) {
     if (seg > 0) {
       const Segment& sg = *x.segment(seg - 1);
       const Item& it = sg.it;
-      named_sync(kPvReady, C::kSync);
+      named_sync(kPvReady + ((i - 1) & 1), C::kSync);
       const bool ok = *reinterpret_cast<volatile int*>(&x.ms()->abort_flag) == 0;
       tc_fence_after();
       // row sums over the key lanes
@@ -974,8 +979,8 @@ __device__ void softmax_warps(const Ctx<R>& x) {
       for (; i < n; ++i) {
         named_sync(kSReady + (i & 1), C::kSync);
         if (i + 2 < n) named_arrive(kSFree + (i & 1), C::kSync);
-        named_arrive(kPReady, C::kSync);
-        named_sync(kPvReady, C::kSync);
+        if constexpr (!C::kPollP) named_arrive(kPReady, C::kSync);
+        named_sync(kPvReady + (i & 1), C::kSync);
       }
       break;
     }
@@ -993,7 +998,6 @@ __device__ void softmax_warps(const Ctx<R>& x) {
     }
 #pragma unroll 1
     for (int k = 0; k < n_seg; ++k, ++i) {
-      if (C::kLockstep && k > 0) named_sync(kPvReady, C::kSync);
       if (i > 0) named_sync(kSReady + (i & 1), C::kSync);
       tc_fence_after();
       const int e_key = e_page == kNoPage ? 0 : e_page;
@@ -1040,7 +1044,7 @@ __device__ void softmax_warps(const Ctx<R>& x) {
 #pragma unroll
       for (int r = 1; r < HR; ++r) over = fmaxf(over, y[r]);
       // the previous PV has to be waited for (a segment's last one was)
-      bool pv_due = !C::kLockstep && k > 0;
+      bool pv_due = k > 0;
       if (named_or(kVote + g, 128, over > 8.f) || unset != 0u) {
         // a new reference for the rows that need one
         float mx = -INFINITY;
@@ -1065,7 +1069,7 @@ __device__ void softmax_warps(const Ctx<R>& x) {
 #pragma unroll
         for (int r = 0; r < HR; ++r) y[r] -= __shfl_sync(0xffffffffu, d, r);
         if (__any_sync(0xffffffffu, f != 1.f)) {
-          if (pv_due) named_sync(kPvReady, C::kSync);
+          if (pv_due) named_sync(kPvReady + ((i - 1) & 1), C::kSync);
           tc_fence_after();
           float fr[HR];
 #pragma unroll
@@ -1108,7 +1112,7 @@ __device__ void softmax_warps(const Ctx<R>& x) {
                       f32_to_e4m3x2((p[2] - b1.x) * kLo, (p[3] - b1.y) * kLo) << 16;
         }
       }
-      if (pv_due) named_sync(kPvReady, C::kSync);  // P's place is free
+      if (pv_due) named_sync(kPvReady + ((i - 1) & 1), C::kSync);  // P's place is free
       unsigned char* stage = x.s() + C::kOffStage + (i & 1) * kStageBytes;
       {
         // 16 rows are one 16-byte unit of the key's 64-byte row, 64-byte swizzle
@@ -1137,7 +1141,11 @@ __device__ void softmax_warps(const Ctx<R>& x) {
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      named_arrive(kPReady, C::kSync);
+      if constexpr (C::kPollP) {
+        if (lane == 0) mbar_arrive(x.bar(kPFull));
+      } else {
+        named_arrive(kPReady, C::kSync);
+      }
       if (i + 1 < n) {
         const TileInfo* next = x.info(i + 1);
         e_page = next->exp[slot];
@@ -1160,7 +1168,7 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, 1)
     ms->status = ms->info = 0u;
     ms->abort_flag = 0;
     for (int b = 0; b < C::kNumBars; ++b)
-      mbar_init(x.bar(b), b == kQFull || b == kOFree ? C::kWarps : 1);
+      mbar_init(x.bar(b), b == kQFull || b == kOFree || b == kPFull ? C::kWarps : 1);
     fence_barrier_init();
     prefetch_tmap(&ml);
     prefetch_tmap(&mr);
@@ -1180,7 +1188,7 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, 1)
     if (warp < C::kWarps) softmax_warps<R>(x);
     else if (warp == C::kWarps) producer<R>(x, &ml, &mr);
     else if (warp == C::kWarps + 1) mma_issuer<R>(x);
-    else relay<R>(x);
+    else relay<R>(x, warp == C::kWarps + 3);
   }
   tc_fence_before();
   __syncthreads();
