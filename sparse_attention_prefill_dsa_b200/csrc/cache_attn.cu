@@ -39,6 +39,7 @@
 // cache_attn_combine joins. The list's length comes from the batch arrays, so
 // each CTA counts it for itself; nothing of it is needed on the host.
 #include <cuda_bf16.h>
+#include <limits.h>
 
 #include "cache.cuh"
 #include "sm100_primitives.cuh"
@@ -183,10 +184,10 @@ struct SegmentWalk {
   }
 };
 
-// Published segments. The producer publishes a segment two tiles before it
+// Published segments. The producer publishes a segment three tiles before it
 // loads its first; a tile's place is loaded again once its PV is done, which
 // every warp has taken part in. So the warp that is furthest behind is at most
-// five tiles, and segments, behind.
+// six tiles, and segments, behind.
 constexpr int kSegSlots = 8;
 static_assert(sizeof(Segment) <= 64, "segment slot");
 
@@ -211,10 +212,10 @@ static_assert(sizeof(Misc) <= 48, "misc");
 
 // mbarriers: what TMA and the tensor cores arrive on, and rare events.
 enum Bars {
-  kFull = 0,              // [2 stages][5 chunks] a tile's chunk has landed
-  kEmpty = 10,            // [2][5] the PV is done with it
-  kSFull = 20,            // [2] QK^T of a tile is done
-  kPvDone = 22,           // PV of a tile is done
+  kFull = 0,              // [2 stages][2 halves] a tile's dims 0-255, 256-511 and rope have landed
+  kEmpty = 4,             // [2][2] the PV is done with them
+  kSFull = 8,             // [2] QK^T of a tile is done
+  kPvDone = 10,           // PV of a tile is done
   kQFull,                 // the segment's Q is written
   kOFree,                 // the segment's O has been read
   kPFull,                 // P of a tile is written (kPollP)
@@ -273,6 +274,10 @@ struct Cfg {
 
 enum Sites { kSiteEmpty = 40, kSiteFull, kSiteSFull, kSitePv, kSiteQ, kSiteO, kSiteSeg, kSiteInfo, kSiteP };
 
+#ifndef POLLNS
+#define POLLNS 20
+#endif
+constexpr unsigned kPollPauseNs = POLLNS;
 constexpr int kNoPage = 1 << 20;
 
 // The kernel's shared memory: a symbol, so that operand addresses are
@@ -536,9 +541,24 @@ __device__ void convert_q(const CacheAttnArgs& a, const Item& it, unsigned char*
 
 // -------------------------------------------------------------------- kernel
 
-// The polling loop of a wait, once for all waits.
+// The polling loop of a wait, once for all waits. Polls read shared memory,
+// which the MMAs keep busy: a warp that polls without a pause holds up the
+// others' (a producer that shared it with three such warps took 570 clocks for
+// each wait, barrier and load of a chunk).
 __device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, Misc* ms, unsigned site) {
-  return mbar_wait(bar, parity, &ms->abort_flag, reinterpret_cast<WsHeader*>(&ms->status), site);
+  const long long t0 = clock64();
+  for (uint32_t i = 1;; ++i) {
+    __nanosleep(kPollPauseNs);
+    if (mbar_test_wait(bar, parity)) return true;
+    if ((i & 63u) == 0u) {
+      if (*reinterpret_cast<volatile int*>(&ms->abort_flag)) return false;
+      if (clock64() - t0 > kWaitLimitCycles) {
+        ms->abort_flag = 1;
+        report(reinterpret_cast<WsHeader*>(&ms->status), kDevTimeout, site);
+        return false;
+      }
+    }
+  }
 }
 
 template <int R>
@@ -558,7 +578,7 @@ struct Ctx {
     return reinterpret_cast<TileInfo*>(cache_attn_smem + Cfg<R>::kOffTile) + (i & 3);
   }
   __device__ __forceinline__ bool wait(int b, uint32_t parity, unsigned site) const {
-    return mbar_try_wait(bar(b), parity) || wait_on(bar(b), parity, ms(), site);
+    return mbar_test_wait(bar(b), parity) || wait_on(bar(b), parity, ms(), site);
   }
   __device__ __forceinline__ bool wait_segment(int seg) const {
     return wait(kSeg + seg % kSegSlots, (seg / kSegSlots) & 1, kSiteSeg);
@@ -607,79 +627,105 @@ __device__ void producer(const Ctx<R>& x, const CUtensorMap* ml, const CUtensorM
       me.first = cta_of_tile(x.ms()->begin - sg.k0, x.ms()->total, gridDim.x, blockIdx.x);
     }
   }
-  // The next tile to plan is tile k of the segment. Its plan: this lane's page
-  // (-1 when no row of the item sees any of it), its first key, whether all
-  // rows see all of it.
-  int k = sg.k0, page = -1, t0 = 0;
-  bool whole = false;
+  // The segment that is being planned, in registers (the walk itself is in
+  // local memory, and reading it for every tile took longer than the loads).
+  const int32_t* table;
+  int k, k1, nst, wt0, t_lo, t_hi, win_lo, sink_hi;
+  auto enter = [&] {
+    table = a.batch.page_table + static_cast<int64_t>(sg.it.b) * a.batch.max_pages;
+    k = sg.k0;
+    k1 = sg.k1;
+    nst = sg.it.nst;
+    wt0 = sg.it.wt0;
+    t_lo = sg.it.t_lo;
+    t_hi = sg.it.t_hi;
+    win_lo = sg.it.win_lo;
+    sink_hi = sg.it.sink_hi;
+  };
+  enter();
+  // A tile's plan: this lane's page as the table has it (kNoPage when no row of
+  // the item sees any of it), its first key, whether all rows see all of it.
+  const int page_shift = 31 - __clz(ps);
+  struct Plan {
+    int page, t0;
+    bool whole;
+  };
   auto plan = [&] {
-    t0 = sg.it.tile(k) * kKeys;
-    whole = t0 + kKeys - 1 <= sg.it.t_lo &&
-            (a.window == 0 || t0 > sg.it.t_hi - a.window || t0 + kKeys <= a.n_sink);
-    page = -1;
-    if (lane < npt) {
-      const int s0 = t0 + lane * ps, s1 = s0 + ps - 1;
-      if (s0 <= sg.it.t_hi && (s1 >= sg.it.win_lo || s0 < sg.it.sink_hi)) {
-        page = __ldg(a.batch.page_table + static_cast<int64_t>(sg.it.b) * a.batch.max_pages + s0 / ps);
-        if (page < 0 || page >= a.cache.n_pages) {
-          x.error(kCacheSitePage);
-          page = -1;
-        }
-      }
-    }
-    if (++k == sg.k1 && sg.next(a)) {
-      k = sg.k0;
+    Plan p;
+    p.t0 = (k < nst ? k : wt0 + k - nst) * kKeys;
+    p.whole = p.t0 + kKeys - 1 <= t_lo &&
+              (a.window == 0 || p.t0 > t_hi - a.window || p.t0 + kKeys <= a.n_sink);
+    p.page = INT_MIN;
+    const int s0 = p.t0 + lane * ps;
+    if (lane < npt && s0 <= t_hi && (s0 + ps > win_lo || s0 < sink_hi))
+      p.page = __ldg(table + (s0 >> page_shift));
+    if (++k == k1 && sg.next(a)) {
+      enter();
       publish();
     }
+    return p;
   };
-  auto tell = [&](int i, int pg, int first, bool all) {
-    const bool has = lane >= npt || pg >= 0;
-    const int e = lane < npt && pg >= 0 ? scale_exp(__ldg(a.cache.scale + pg)) : kNoPage;
-    const bool full = all && __all_sync(0xffffffffu, has);
+  auto in_pool = [&](int page) { return page >= 0 && page < a.cache.n_pages; };
+  auto scale_of = [&](const Plan& p) { return in_pool(p.page) ? __ldg(a.cache.scale + p.page) : 0.f; };
+  auto tell = [&](int i, const Plan& p, float sc) {
+    const bool has = in_pool(p.page);
+    if (!has && p.page != INT_MIN) x.error(kCacheSitePage);
+    const bool full = __all_sync(0xffffffffu, has || lane >= npt) && p.whole;
     TileInfo* out = x.info(i);
-    if (lane < npt) out->exp[lane] = e;
+    if (lane < npt) out->exp[lane] = has ? scale_exp(sc) : kNoPage;
     if (lane == 0) {
-      out->t0 = first;
+      out->t0 = p.t0;
       out->masked = !full;
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(x.bar(kInfo + (i & 3)));
   };
-  plan();
+  // Tile i is loaded, tile i + 1 has its pages and gets its scales, tile i + 2
+  // gets its pages.
+  Plan now = plan(), next = now, after = now;
+  if (n > 1) next = plan();
+  float sc0 = 0.f;
   bool ok = true;
   int c_failed = 0, i = 0;
+#pragma unroll 1
   for (; i < n && ok; ++i) {
-    const int pg = page, first = t0;
-    const bool all = whole;
-    if (i + 1 < n) plan();
-    const int bytes = __popc(__ballot_sync(0xffffffffu, pg >= 0)) * ps;
+    if (i + 2 < n) after = plan();
+    const int pg = in_pool(now.page) ? now.page : -1;
+    const int bytes = __popc(__ballot_sync(0xffffffffu, pg >= 0)) << page_shift;
     const int st = i & 1;
     unsigned char* dst = x.s() + Cfg<R>::kOffStage + st * kStageBytes;
-#pragma unroll 1
-    for (int c = 0; c < 5; ++c) {
-      if (i >= 2) ok = x.wait(kEmpty + 5 * st + c, ((i >> 1) - 1) & 1, kSiteEmpty);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      if (i >= 2 && ok) ok = x.wait(kEmpty + 2 * st + c, ((i >> 1) - 1) & 1, kSiteEmpty);
       ok = __all_sync(0xffffffffu, ok);
-      if (!ok) {
-        c_failed = c;
-        break;
-      }
-      uint64_t* full = x.bar(kFull + 5 * st + c);
-      if (lane == 0) mbar_arrive_expect_tx(full, bytes * (c < 4 ? 128 : kDR));
-      __syncwarp();
-      if (pg >= 0) {
-        if (c < 4) tma_load_3d(dst + c * kChunkBytes + lane * ps * 128, ml, c * 128, 0, pg, full);
-        else tma_load_3d(dst + kRopeOff + lane * ps * kDR, mr, 0, 0, pg, full);
+      if (ok) {
+        uint64_t* full = x.bar(kFull + 2 * st + c);
+        if (lane == 0) mbar_arrive_expect_tx(full, bytes * (c == 0 ? 256 : 256 + kDR));
+        __syncwarp();
+        if (pg >= 0) {
+          unsigned char* at = dst + 2 * c * kChunkBytes + lane * ps * 128;
+          tma_load_3d(at, ml, c * 256, 0, pg, full);
+          tma_load_3d(at + kChunkBytes, ml, c * 256 + 128, 0, pg, full);
+          if (c == 1) tma_load_3d(dst + kRopeOff + lane * ps * kDR, mr, 0, 0, pg, full);
+        }
+        c_failed = c + 1;
+      } else if (c == 0) {
+        c_failed = 0;
       }
     }
-    if (i == 0) tell(0, pg, first, all);
-    if (i + 1 < n) tell(i + 1, page, t0, whole);
+    if (i == 0) sc0 = scale_of(now);
+    const float sc1 = i + 1 < n ? scale_of(next) : 0.f;
+    if (i == 0) tell(0, now, sc0);
+    if (i + 1 < n) tell(i + 1, next, sc1);
+    now = next;
+    next = after;
   }
   if (!ok && lane == 0) {
     // Let the copies in flight land before the block ends: tile i - 1 was
-    // begun up to chunk c_failed, the one before it in full.
-    for (int c = 0; c < 5; ++c)
+    // begun up to half c_failed, the one before it in full.
+    for (int c = 0; c < 2; ++c)
       for (int j = max(i - 3, 0); j < i; ++j)
-        if (j < i - 1 || c < c_failed) drain_wait(x.bar(kFull + 5 * (j & 1) + c), (j >> 1) & 1);
+        if (j < i - 1 || c < c_failed) drain_wait(x.bar(kFull + 2 * (j & 1) + c), (j >> 1) & 1);
   }
 }
 
@@ -690,6 +736,7 @@ __device__ __noinline__ int wait_either(uint64_t* a, uint32_t pa, uint64_t* b, u
   const long long t0 = clock64();
   for (uint32_t i = 1;; ++i) {
     int r = mbar_test_wait(a, pa) ? 1 : mbar_test_wait(b, pb) ? 2 : 0;
+    if (r == 0) __nanosleep(kPollPauseNs);
     if (r == 0 && (i & 63u) == 0u) {
       if (*reinterpret_cast<volatile int*>(&ms->abort_flag)) r = 3;
       else if (clock64() - t0 > kWaitLimitCycles) {
@@ -735,7 +782,7 @@ __device__ void mma_issuer(const Ctx<R>& x) {
   for (;;) {
     bool pv = v < q && (q == n || q - v == 2 || left == 0);
     if (C::kPollP && !pv && v < q) {
-      const int r = ok ? wait_either(x.bar(kFull + 5 * (q & 1) + 4), (q >> 1) & 1, x.bar(kPFull),
+      const int r = ok ? wait_either(x.bar(kFull + 2 * (q & 1) + 1), (q >> 1) & 1, x.bar(kPFull),
                                      v & 1, x.ms(), kSiteP) : 0;
       ok = ok && r != 0;
       pv = r == 2;
@@ -764,9 +811,8 @@ __device__ void mma_issuer(const Ctx<R>& x) {
             for (int kk = 0; kk < 4; ++kk)
               mma_f8_ss(d, av + ((kk * 4096) >> 4), dp + ((kk * 2048) >> 4), C::kIdescPV, 1u);
           }
-          mma_commit(x.bar(kEmpty + 5 * (i & 1) + c));  // each chunk goes as its block is done
+          if (c & 1) mma_commit(x.bar(kEmpty + 2 * (i & 1) + c / 2));  // a half goes as its blocks are done
         }
-        mma_commit(x.bar(kEmpty + 5 * (i & 1) + 4));
         mma_commit(x.bar(kPvDone));
       }
       __syncwarp();
@@ -785,20 +831,18 @@ __device__ void mma_issuer(const Ctx<R>& x) {
       const uint64_t so = static_cast<uint64_t>((i & 1) * kStageBytes) >> 4;
       const uint32_t d = C::kTmemS + 2 * R * (i & 1);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        ok = ok && x.wait(kFull + 5 * (i & 1) + c, (i >> 1) & 1, kSiteFull);
+      for (int c = 0; c < 2; ++c) {
+        ok = ok && x.wait(kFull + 2 * (i & 1) + c, (i >> 1) & 1, kSiteFull);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
         if (ok && lead) {
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_f8_ss(d, dk + so + ((c * kChunkBytes + ks * 32) >> 4),
-                      dq + ((c * C::kQChunk + ks * 32) >> 4), C::kIdescQK, c > 0 || ks > 0);
+          for (int ks = 0; ks < 8; ++ks)
+            mma_f8_ss(d, dk + so + (((2 * c + ks / 4) * kChunkBytes + ks % 4 * 32) >> 4),
+                      dq + (((2 * c + ks / 4) * C::kQChunk + ks % 4 * 32) >> 4), C::kIdescQK,
+                      c > 0 || ks > 0);
         }
       }
-      ok = ok && x.wait(kFull + 5 * (i & 1) + 4, (i >> 1) & 1, kSiteFull);
-      ok = __all_sync(0xffffffffu, ok);
-      tc_fence_after();
       if (ok && lead) {
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
@@ -1128,7 +1172,7 @@ __device__ void softmax_warps(const Ctx<R>& x) {
         // have landed (QK^T read them); waiting on them orders the writes.
 #pragma unroll 1
         for (int c = g; c < 4; c += C::kGroups) {
-          const bool there = x.wait(kFull + 5 * (i & 1) + c, (i >> 1) & 1, kSiteFull);
+          const bool there = x.wait(kFull + 2 * (i & 1) + c / 2, (i >> 1) & 1, kSiteFull);
           if (gone && there) {
             // (lanes start at different units, for different banks)
 #pragma unroll
