@@ -88,6 +88,25 @@ struct Item {
   }
 };
 
+// The keys that the rows [i0, i1] of a sequence (token * n_heads + head, its
+// first new token at position `first`) see, and the tiles with them.
+struct KeyRange {
+  int t_lo, t_hi, win_lo, sink_hi, nst, wt0, nt;
+};
+
+__device__ __forceinline__ KeyRange key_range(const CacheAttnArgs& a, int first, unsigned i0,
+                                              unsigned i1) {
+  KeyRange k;
+  k.t_lo = first + static_cast<int>(i0 / static_cast<unsigned>(a.n_heads));
+  k.t_hi = first + static_cast<int>(i1 / static_cast<unsigned>(a.n_heads));
+  k.win_lo = a.window > 0 ? max(0, k.t_lo - a.window + 1) : 0;
+  k.sink_hi = a.window > 0 ? min(a.n_sink, k.win_lo) : 0;
+  k.nst = (k.sink_hi + kKeys - 1) / kKeys;
+  k.wt0 = max(k.win_lo / kKeys, k.nst);
+  k.nt = k.nst + k.t_hi / kKeys - k.wt0 + 1;
+  return k;
+}
+
 template <int R>
 __device__ __forceinline__ int64_t slots_of(const CacheAttnArgs& a) {
   return static_cast<int64_t>(a.batch.n_tok) * a.n_heads / R + a.batch.n_seq;
@@ -130,13 +149,14 @@ struct ItemWalk {
     it.n_rows = static_cast<int>(min(static_cast<int64_t>(R), rows - it.i0));
     it.row = r.tok0 * a.n_heads + it.i0;
     it.first = r.len - r.n;
-    it.t_lo = it.first + it.i0 / a.n_heads;
-    it.t_hi = it.first + (it.i0 + it.n_rows - 1) / a.n_heads;
-    it.win_lo = a.window > 0 ? max(0, it.t_lo - a.window + 1) : 0;
-    it.sink_hi = a.window > 0 ? min(a.n_sink, it.win_lo) : 0;
-    it.nst = (it.sink_hi + kKeys - 1) / kKeys;
-    it.wt0 = max(it.win_lo / kKeys, it.nst);
-    it.nt = it.nst + it.t_hi / kKeys - it.wt0 + 1;
+    const KeyRange k = key_range(a, it.first, it.i0, it.i0 + it.n_rows - 1);
+    it.t_lo = k.t_lo;
+    it.t_hi = k.t_hi;
+    it.win_lo = k.win_lo;
+    it.sink_hi = k.sink_hi;
+    it.nst = k.nst;
+    it.wt0 = k.wt0;
+    it.nt = k.nt;
     return it.nt;
   }
 };
@@ -274,10 +294,7 @@ struct Cfg {
 
 enum Sites { kSiteEmpty = 40, kSiteFull, kSiteSFull, kSitePv, kSiteQ, kSiteO, kSiteSeg, kSiteInfo, kSiteP };
 
-#ifndef POLLNS
-#define POLLNS 20
-#endif
-constexpr unsigned kPollPauseNs = POLLNS;
+constexpr unsigned kPollPauseNs = 20;  // (0 to 100 measured alike)
 constexpr int kNoPage = 1 << 20;
 
 // The kernel's shared memory: a symbol, so that operand addresses are
@@ -375,14 +392,26 @@ __device__ void schedule(const CacheAttnArgs& a, Misc* ms, long long* scan, Segm
   const int64_t slots = __syncthreads_or(bad) ? 0 : slots_of<R>(a);
   const int64_t per = (slots + kThreads - 1) / kThreads;
   const int64_t s0 = min(slots, tid * per), s1 = min(slots, s0 + per);
-  ItemWalk<R> w;
-  Item it;
   long long sum = 0;
   if (s0 < s1) {
-    w.seek(a, s0);
+    int b = seq_of_slot(a.batch, s0, a.n_heads, ItemWalk<R>::kShift, 1);
+    SeqRange r = seq_range(a.batch, a.cache.page_size, b);
+    int64_t start = slot_start(a.batch, b, a.n_heads, ItemWalk<R>::kShift, 1);
+    int64_t stop = b + 1 < a.batch.n_seq
+                       ? slot_start(a.batch, b + 1, a.n_heads, ItemWalk<R>::kShift, 1) : INT64_MAX;
+#pragma unroll 1
     for (int64_t s = s0; s < s1; ++s) {
-      sum += w.item(a, it);
-      if (s + 1 < s1) w.next(a);
+      while (s >= stop) {
+        ++b;
+        r = seq_range(a.batch, a.cache.page_size, b);
+        start = stop;
+        stop = b + 1 < a.batch.n_seq
+                   ? slot_start(a.batch, b + 1, a.n_heads, ItemWalk<R>::kShift, 1) : INT64_MAX;
+      }
+      const int64_t i0 = (s - start) * R, rows = static_cast<int64_t>(r.n) * a.n_heads;
+      if (i0 < rows)
+        sum += key_range(a, r.len - r.n, static_cast<unsigned>(i0),
+                         static_cast<unsigned>(min(i0 + R, rows)) - 1).nt;
     }
   }
   long long inc = sum;
@@ -403,20 +432,20 @@ __device__ void schedule(const CacheAttnArgs& a, Misc* ms, long long* scan, Segm
   const long long lo = before + inc - sum;
   if (begin < end && lo <= begin && begin < lo + sum) {
     // this thread's: it publishes the CTA's first segment
+    ItemWalk<R> w;
+    Item it;
     long long at = lo;
-    int n = static_cast<int>(sum);
-    if (s1 - s0 > 1) {
-      w.seek(a, s0);
-      while (at + (n = w.item(a, it)) <= begin) {
-        at += n;
-        w.next(a);
-      }
+    int n;
+    w.seek(a, s0);
+    while (at + (n = w.item(a, it)) <= begin) {
+      at += n;
+      w.next(a);
     }
     first->it = it;
     first->k0 = static_cast<int>(begin - at);
     first->k1 = static_cast<int>(min(static_cast<long long>(it.nt), first->k0 + end - begin));
     first->more = first->k1 - first->k0 < end - begin;
-    ms->slot = s0 + (s1 - s0 > 1 ? w.slot - s0 : 0);
+    ms->slot = w.slot;
   }
   if (tid == 0) {
     ms->n_tiles = end - begin;
@@ -699,6 +728,8 @@ __device__ void producer(const Ctx<R>& x, const CUtensorMap* ml, const CUtensorM
       if (i >= 2 && ok) ok = x.wait(kEmpty + 2 * st + c, ((i >> 1) - 1) & 1, kSiteEmpty);
       ok = __all_sync(0xffffffffu, ok);
       if (ok) {
+        // (not before the place is free: until then the barrier may still be
+        // waiting for what was loaded there last)
         uint64_t* full = x.bar(kFull + 2 * st + c);
         if (lane == 0) mbar_arrive_expect_tx(full, bytes * (c == 0 ? 256 : 256 + kDR));
         __syncwarp();
