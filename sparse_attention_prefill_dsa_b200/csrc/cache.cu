@@ -113,16 +113,18 @@ __device__ void rescale_codes(uint8_t* p, int n16, float f) {
   }
 }
 
-// Sixteen-byte units of a latent row (8 elements) and pairs of a rope row are
-// dealt over the CTA so that each thread holds kUnits and kPairs of them: at
-// most eight and four, in 64 registers, so that an SM runs 1,024 threads (with
-// 256 threads a page of 64 they took 128, and a chunk of 8,192 tokens 33 us).
+// A page's rows are read twice, for the scale and for the codes (the second
+// time from L2): the registers they would take are better given to more
+// threads, which the queries' CTAs of the same launch, most of the bytes, need.
+// The rotated rope stays in registers, four pairs of float64 a thread (with
+// eight, on half the threads, a page took so long that a chunk of 8,192 tokens
+// took 31 us instead of 24).
 template <int DC, int DR, int PS>
 struct AppendCfg {
   static constexpr int kThr = PS <= 32 ? 256 : 8 * PS;
   static constexpr int kMinBlocks = 1024 / kThr;
-  static constexpr int kQTokens = kThr / 64;  // tokens of a q CTA
-  static constexpr int kRowUnits = DC / 8;
+  static constexpr int kMaxQTokens = 16;      // tokens of a q CTA, at most
+  static constexpr int kRowUnits = DC / 8;    // 16-byte units of a latent row
   static constexpr int kUnits = (PS * kRowUnits + kThr - 1) / kThr;
   static constexpr int kRowPairs = DR / 2;
   static constexpr int kPairs = (PS * kRowPairs + kThr - 1) / kThr;
@@ -165,15 +167,25 @@ __device__ void append_page(const AppendArgs& a, int64_t slot) {
   const float old_scale = __ldg(a.cache.scale + page);
   if (threadIdx.x == 0) s_exp = kCacheMinExp;
 
-  uint4 lat[C::kUnits];
   int need = kCacheMinExp;
-#pragma unroll
-  for (int u = 0; u < C::kUnits; ++u) {
+  auto unit = [&](int u) {
     const int x = threadIdx.x + u * C::kThr, row = x / C::kRowUnits;
-    lat[u] = make_uint4(0u, 0u, 0u, 0u);
-    if (row >= r0 && row < r1)
-      lat[u] = __ldg(reinterpret_cast<const uint4*>(a.latent + (tok + row) * a.ld_latent) +
-                     x % C::kRowUnits);
+    return row >= r0 && row < r1
+               ? __ldg(reinterpret_cast<const uint4*>(a.latent + (tok + row) * a.ld_latent) +
+                       x % C::kRowUnits)
+               : make_uint4(0u, 0u, 0u, 0u);
+  };
+  {
+    uint32_t top = 0u;  // the largest |x|: bf16 magnitudes order as integers
+#pragma unroll 8
+    for (int u = 0; u < C::kUnits; ++u) {
+      const uint4 v = unit(u);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        top = max(top, max((w[e] & 0x7FFFu) << 16, w[e] & 0x7FFF0000u));
+    }
+    need = max(need, need_exp_f32(__uint_as_float(top)));
   }
   double2 rot[C::kPairs];
 #pragma unroll
@@ -189,15 +201,6 @@ __device__ void append_page(const AppendArgs& a, int64_t slot) {
              &cs);
       rot[u] = make_double2(v * cs - w * sn, w * cs + v * sn);
       need = max(need, max(need_exp_f64(rot[u].x), need_exp_f64(rot[u].y)));
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < C::kUnits; ++u) {
-    const uint32_t w[4] = {lat[u].x, lat[u].y, lat[u].z, lat[u].w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 f = bf16x2(w[e]);
-      need = max(need, max(need_exp_f32(f.x), need_exp_f32(f.y)));
     }
   }
   need = __reduce_max_sync(0xffffffffu, need);
@@ -219,12 +222,12 @@ __device__ void append_page(const AppendArgs& a, int64_t slot) {
   }
   const float inv = pow2f(-e_new);
   if (threadIdx.x == 0) a.cache.scale[page] = pow2f(e_new);
-#pragma unroll
+#pragma unroll 8
   for (int u = 0; u < C::kUnits; ++u) {
     const int x = threadIdx.x + u * C::kThr, row = x / C::kRowUnits;
     if (row < r0 || row >= r1) continue;
-    const float2 f0 = bf16x2(lat[u].x), f1 = bf16x2(lat[u].y), f2 = bf16x2(lat[u].z),
-                 f3 = bf16x2(lat[u].w);
+    const uint4 w = unit(u);
+    const float2 f0 = bf16x2(w.x), f1 = bf16x2(w.y), f2 = bf16x2(w.z), f3 = bf16x2(w.w);
     uint2 v;
     v.x = f32_to_e4m3x2(f0.x * inv, f0.y * inv) | f32_to_e4m3x2(f1.x * inv, f1.y * inv) << 16;
     v.y = f32_to_e4m3x2(f2.x * inv, f2.y * inv) | f32_to_e4m3x2(f3.x * inv, f3.y * inv) << 16;
@@ -300,20 +303,20 @@ struct QItem {
   }
 };
 
-// Rotates the queries' rope of kQTokens tokens. A thread's first items are
-// loaded before the angles are worked out.
-template <int DC, int DR, int kQTokens>
-__device__ void rotate_q(const AppendArgs& a, int64_t tok0) {
-  __shared__ float2 s_cs[kQTokens * (DR / 2)];
-  __shared__ int s_pos[kQTokens];
+// Rotates the queries' rope of n_tok tokens. A thread's first items are loaded
+// before the angles are worked out.
+template <int DC, int DR, int kMaxTokens>
+__device__ void rotate_q(const AppendArgs& a, int64_t tok0, int n_tok) {
+  __shared__ float2 s_cs[kMaxTokens * (DR / 2)];
+  __shared__ int s_pos[kMaxTokens];
   constexpr int kPerHead = DR / 16, kAhead = 2;
-  const int items = kQTokens * a.n_heads * kPerHead;
+  const int items = n_tok * a.n_heads * kPerHead;
   QItem<DC, DR> it[kAhead];
   bool has[kAhead];
 #pragma unroll
   for (int i = 0; i < kAhead; ++i)
     has[i] = it[i].load(a, tok0, threadIdx.x + i * blockDim.x, items, s_cs);
-  if (threadIdx.x < kQTokens) {
+  if (threadIdx.x < n_tok) {
     const int64_t tok = tok0 + threadIdx.x;
     int pos = -1;
     if (tok < a.batch.n_tok) {
@@ -326,7 +329,7 @@ __device__ void rotate_q(const AppendArgs& a, int64_t tok0) {
     s_pos[threadIdx.x] = pos;
   }
   __syncthreads();
-  for (int x = threadIdx.x; x < kQTokens * (DR / 2); x += blockDim.x) {
+  for (int x = threadIdx.x; x < n_tok * (DR / 2); x += blockDim.x) {
     double sn, cs;
     sincos(static_cast<double>(s_pos[x / (DR / 2)]) *
                static_cast<double>(__ldg(a.inv_freq + x % (DR / 2))), &sn, &cs);
@@ -345,20 +348,26 @@ __device__ void rotate_q(const AppendArgs& a, int64_t tok0) {
 
 template <int DC, int DR, int PS>
 __global__ void __launch_bounds__(AppendCfg<DC, DR, PS>::kThr, AppendCfg<DC, DR, PS>::kMinBlocks)
-    cache_append_kernel(const __grid_constant__ AppendArgs a, int64_t page_slots) {
+    cache_append_kernel(const __grid_constant__ AppendArgs a, int64_t page_slots, int q_tokens) {
   const int64_t x = blockIdx.x;
-  if (x < page_slots) append_page<DC, DR, PS>(a, x);
-  else if (x == page_slots) append_check(a);
-  else rotate_q<DC, DR, AppendCfg<DC, DR, PS>::kQTokens>(a, (x - page_slots - 1) * AppendCfg<DC, DR, PS>::kQTokens);
+  if (x < page_slots)
+    append_page<DC, DR, PS>(a, x);
+  else if (x == page_slots)
+    append_check(a);
+  else
+    rotate_q<DC, DR, AppendCfg<DC, DR, PS>::kMaxQTokens>(a, (x - page_slots - 1) * q_tokens, q_tokens);
 }
 
 template <int DC, int DR, int PS>
 cudaError_t launch_append_t(const AppendArgs& a, cudaStream_t st) {
-  constexpr int kQTokens = AppendCfg<DC, DR, PS>::kQTokens;
+  using C = AppendCfg<DC, DR, PS>;
   const int64_t pages = a.batch.n_tok / PS + 2ll * a.batch.n_seq;
-  const int64_t q = a.q ? (static_cast<int64_t>(a.batch.n_tok) + kQTokens - 1) / kQTokens : 0;
-  cache_append_kernel<DC, DR, PS><<<static_cast<unsigned>(pages + 1 + q),
-                                    AppendCfg<DC, DR, PS>::kThr, 0, st>>>(a, pages);
+  // two items a thread: the loads that are in flight while the angles are worked out
+  int q_tokens = 1;
+  while (q_tokens < C::kMaxQTokens && 2 * q_tokens * a.n_heads * (DR / 16) <= 2 * C::kThr) q_tokens *= 2;
+  const int64_t q = a.q ? (static_cast<int64_t>(a.batch.n_tok) + q_tokens - 1) / q_tokens : 0;
+  cache_append_kernel<DC, DR, PS><<<static_cast<unsigned>(pages + 1 + q), C::kThr, 0, st>>>(
+      a, pages, q_tokens);
   return cudaGetLastError();
 }
 

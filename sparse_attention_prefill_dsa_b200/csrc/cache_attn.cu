@@ -107,6 +107,24 @@ __device__ __forceinline__ KeyRange key_range(const CacheAttnArgs& a, int first,
   return k;
 }
 
+__device__ __forceinline__ Item make_item(const CacheAttnArgs& a, int b, const SeqRange& r, int i0,
+                                          int n_rows, const KeyRange& k) {
+  Item it;
+  it.b = b;
+  it.i0 = i0;
+  it.n_rows = n_rows;
+  it.row = r.tok0 * a.n_heads + i0;
+  it.first = r.len - r.n;
+  it.t_lo = k.t_lo;
+  it.t_hi = k.t_hi;
+  it.win_lo = k.win_lo;
+  it.sink_hi = k.sink_hi;
+  it.nst = k.nst;
+  it.wt0 = k.wt0;
+  it.nt = k.nt;
+  return it;
+}
+
 template <int R>
 __device__ __forceinline__ int64_t slots_of(const CacheAttnArgs& a) {
   return static_cast<int64_t>(a.batch.n_tok) * a.n_heads / R + a.batch.n_seq;
@@ -144,19 +162,9 @@ struct ItemWalk {
     const int64_t rb = slot - start;
     const int64_t rows = static_cast<int64_t>(r.n) * a.n_heads;
     if (rb < 0 || rb * R >= rows) return 0;
-    it.b = b;
-    it.i0 = static_cast<int>(rb * R);
-    it.n_rows = static_cast<int>(min(static_cast<int64_t>(R), rows - it.i0));
-    it.row = r.tok0 * a.n_heads + it.i0;
-    it.first = r.len - r.n;
-    const KeyRange k = key_range(a, it.first, it.i0, it.i0 + it.n_rows - 1);
-    it.t_lo = k.t_lo;
-    it.t_hi = k.t_hi;
-    it.win_lo = k.win_lo;
-    it.sink_hi = k.sink_hi;
-    it.nst = k.nst;
-    it.wt0 = k.wt0;
-    it.nt = k.nt;
+    const int i0 = static_cast<int>(rb * R);
+    const int n_rows = static_cast<int>(min(static_cast<int64_t>(R), rows - i0));
+    it = make_item(a, b, r, i0, n_rows, key_range(a, r.len - r.n, i0, i0 + n_rows - 1));
     return it.nt;
   }
 };
@@ -392,28 +400,40 @@ __device__ void schedule(const CacheAttnArgs& a, Misc* ms, long long* scan, Segm
   const int64_t slots = __syncthreads_or(bad) ? 0 : slots_of<R>(a);
   const int64_t per = (slots + kThreads - 1) / kThreads;
   const int64_t s0 = min(slots, tid * per), s1 = min(slots, s0 + per);
-  long long sum = 0;
-  if (s0 < s1) {
-    int b = seq_of_slot(a.batch, s0, a.n_heads, ItemWalk<R>::kShift, 1);
+  // The slots [s0, s1) in order; `at` gets a slot's sequence, its first row
+  // there and its keys, and tells whether to stop.
+  auto walk = [&](auto at) {
+    if (s0 >= s1) return;
+    constexpr int kShift = ItemWalk<R>::kShift;
+    int b = seq_of_slot(a.batch, s0, a.n_heads, kShift, 1);
     SeqRange r = seq_range(a.batch, a.cache.page_size, b);
-    int64_t start = slot_start(a.batch, b, a.n_heads, ItemWalk<R>::kShift, 1);
-    int64_t stop = b + 1 < a.batch.n_seq
-                       ? slot_start(a.batch, b + 1, a.n_heads, ItemWalk<R>::kShift, 1) : INT64_MAX;
+    int64_t start = slot_start(a.batch, b, a.n_heads, kShift, 1);
+    auto stop_of = [&] {
+      return b + 1 < a.batch.n_seq ? slot_start(a.batch, b + 1, a.n_heads, kShift, 1) : INT64_MAX;
+    };
+    int64_t stop = stop_of();
 #pragma unroll 1
     for (int64_t s = s0; s < s1; ++s) {
       while (s >= stop) {
         ++b;
         r = seq_range(a.batch, a.cache.page_size, b);
         start = stop;
-        stop = b + 1 < a.batch.n_seq
-                   ? slot_start(a.batch, b + 1, a.n_heads, ItemWalk<R>::kShift, 1) : INT64_MAX;
+        stop = stop_of();
       }
       const int64_t i0 = (s - start) * R, rows = static_cast<int64_t>(r.n) * a.n_heads;
-      if (i0 < rows)
-        sum += key_range(a, r.len - r.n, static_cast<unsigned>(i0),
-                         static_cast<unsigned>(min(i0 + R, rows)) - 1).nt;
+      if (i0 < rows) {
+        const int n_rows = static_cast<int>(min(static_cast<int64_t>(R), rows - i0));
+        const KeyRange k = key_range(a, r.len - r.n, static_cast<unsigned>(i0),
+                                     static_cast<unsigned>(i0) + n_rows - 1);
+        if (at(s, b, r, static_cast<int>(i0), n_rows, k)) return;
+      }
     }
-  }
+  };
+  long long sum = 0;
+  walk([&](int64_t, int, const SeqRange&, int, int, const KeyRange& k) {
+    sum += k.nt;
+    return false;
+  });
   long long inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -432,20 +452,19 @@ __device__ void schedule(const CacheAttnArgs& a, Misc* ms, long long* scan, Segm
   const long long lo = before + inc - sum;
   if (begin < end && lo <= begin && begin < lo + sum) {
     // this thread's: it publishes the CTA's first segment
-    ItemWalk<R> w;
-    Item it;
-    long long at = lo;
-    int n;
-    w.seek(a, s0);
-    while (at + (n = w.item(a, it)) <= begin) {
-      at += n;
-      w.next(a);
-    }
-    first->it = it;
-    first->k0 = static_cast<int>(begin - at);
-    first->k1 = static_cast<int>(min(static_cast<long long>(it.nt), first->k0 + end - begin));
-    first->more = first->k1 - first->k0 < end - begin;
-    ms->slot = w.slot;
+    long long done = lo;
+    walk([&](int64_t slot, int b, const SeqRange& r, int i0, int n_rows, const KeyRange& k) {
+      if (done + k.nt <= begin) {
+        done += k.nt;
+        return false;
+      }
+      first->it = make_item(a, b, r, i0, n_rows, k);
+      first->k0 = static_cast<int>(begin - done);
+      first->k1 = static_cast<int>(min(static_cast<long long>(k.nt), first->k0 + end - begin));
+      first->more = first->k1 - first->k0 < end - begin;
+      ms->slot = slot;
+      return true;
+    });
   }
   if (tid == 0) {
     ms->n_tiles = end - begin;
