@@ -1306,24 +1306,27 @@ constexpr int kCombineBlocks = 8;  // per SM
 // Parts of an item up to which a warp joins a whole row by itself.
 constexpr int kFewParts = 4;
 
-// The weights 2^(m_j - M) of one query row's parts (lane j of a warp, or
-// s_w[j] where there are more than 32) and the sum of the weighted l.
+// The weights 2^(m_j - M) of one query row's parts (part 32 i + lane in w[i])
+// and the sum of the weighted l. All loads at once: one latency.
+template <int kRounds>
 struct RowParts {
-  float w, mx, sum;
+  float w[kRounds], mx, sum;
   template <class Part>
-  __device__ __forceinline__ void load(const float2* part_ml, int n, float* s_w, Part part) {
+  __device__ __forceinline__ void load(const float2* part_ml, int n, Part part) {
     const int lane = threadIdx.x & 31;
-    mx = -INFINITY;
-#pragma unroll 1
-    for (int j = lane; j < n; j += 32) mx = fmaxf(mx, __ldcg(part_ml + part(j)).x);
+    float2 ml[kRounds];
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i)
+      ml[i] = 32 * i + lane < n ? __ldcg(part_ml + part(32 * i + lane)) : make_float2(-INFINITY, 0.f);
+    mx = ml[0].x;
+#pragma unroll
+    for (int i = 1; i < kRounds; ++i) mx = fmaxf(mx, ml[i].x);
     mx = warp_max(mx);
-    w = sum = 0.f;
-#pragma unroll 1
-    for (int j = lane; j < n; j += 32) {
-      const float2 ml = __ldcg(part_ml + part(j));
-      w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - mx);
-      sum += w * ml.y;
-      if (s_w) s_w[j] = w;
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+      w[i] = ml[i].x == -INFINITY ? 0.f : exp2f(ml[i].x - mx);
+      sum += w[i] * ml[i].y;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -1419,15 +1422,15 @@ __global__ void __launch_bounds__(kCombineThreads)
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[j][e] = __ldcg(src + 32 * e + lane);
       }
-    RowParts rp;
-    rp.load(p.part_ml, n, nullptr, part);
+    RowParts<1> rp;
+    rp.load(p.part_ml, n, part);
     const int64_t row = static_cast<int64_t>(me.z) + r;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int j = 0; j < kFewParts; ++j) {
-        const float f = __shfl_sync(0xffffffffu, rp.w, j);
+        const float f = __shfl_sync(0xffffffffu, rp.w[0], j);
         if (j < n) add_part(acc, f, v[j][e]);
       }
       store_bf16x4(p.a.out + row * kDC + 128 * e + 4 * lane, acc, rp.inv());
@@ -1439,20 +1442,33 @@ __global__ void __launch_bounds__(kCombineThreads)
     const int r = (u >> 2) % R, quarter = u & 3, c0 = me.y, n = me.x - c0 + 1;
     if (r >= me.w) continue;
     auto part = [&](int j) { return (2ll * (c0 + j) + (j == 0 ? 1 : 0)) * R + r; };
-    RowParts rp;
-    rp.load(p.part_ml, n, s_w[warp], part);
-    __syncwarp();
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-    for (int j0 = warp; j0 < n; j0 += 32) {
-      float4 v[8];
+    // eight parts ahead, the first eight before the weights are known
+    auto fetch = [&](float4(&v)[8], int j0) {
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         v[k] = j0 + 4 * k < n ? __ldcg(reinterpret_cast<const float4*>(
                                            p.part_o + part(j0 + 4 * k) * kDC + quarter * 128) + lane)
                               : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    float4 v[8];
+    fetch(v, warp);
+    RowParts<kRounds> rp;
+    rp.load(p.part_ml, n, part);
+    __syncwarp();
 #pragma unroll
-      for (int k = 0; k < 8; ++k) add_part(acc, j0 + 4 * k < n ? s_w[warp][j0 + 4 * k] : 0.f, v[k]);
+    for (int i = 0; i < kRounds; ++i)
+      if (32 * i + lane < n) s_w[warp][32 * i + lane] = rp.w[i];
+    __syncwarp();
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int j0 = warp; j0 < n; j0 += 32) {
+      float4 next[8];
+      fetch(next, j0 + 32);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (j0 + 4 * k < n) add_part(acc, s_w[warp][j0 + 4 * k], v[k]);
+        v[k] = next[k];
+      }
     }
     if (warp > 0) s_acc[warp - 1][lane] = acc;
     __syncthreads();
