@@ -13,8 +13,10 @@
 // The queries' rope is rotated by CTAs of its own, a few tokens each: the
 // angle in float64, once for each token and pair, cos and sin rounded to float32
 // for the heads, whose outputs are bf16 (8 bits).
-// Bound: the bytes of a prefill chunk (most of them the queries' rope), the
-// chain of dependent loads (batch arrays, page table, rows) of a decode step.
+// Bound: the bytes of a prefill chunk, most of them the queries' rope (8,192
+// tokens with 32 heads 22.6 us, 3.6 TB/s; the angles' chain between a CTA's
+// loads and stores keeps it from the copy rate), the chain of dependent loads
+// (batch arrays, page table, rows) of a decode step (7.2 us of kernel, alone).
 //
 // One more CTA checks the batch arrays and the page table entries that the
 // call uses, and is the only one that writes the status word: the others skip
@@ -395,7 +397,9 @@ struct GatherArgs {
 
 // A thread turns 16 codes (one 16-byte load) into 32 bytes of bf16 (one
 // 32-byte store), eight rows of the same column for eight loads in flight.
-// Bound: bytes (576 read and 1,152 written a row).
+// Bound: bytes, 576 read and 1,152 written a row (17,408 rows 8.2 us, most of
+// it the launch; 130,995 rows 43 us, 5.2 TB/s; with four loads in flight and
+// 16-byte stores 50 us).
 template <int DC, int DR>
 struct GatherCfg {
   static constexpr int kCols = (DC + DR) / 16;                  // 36 (5)

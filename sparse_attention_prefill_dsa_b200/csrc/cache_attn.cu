@@ -29,15 +29,33 @@
 // where the bytes bound; R = 64 else (P's lo and hi passes onto one O, N = 64),
 // which shares the loads between twice as many rows. Shared memory: Q 36 or
 // 72 KB, two tiles of 72 KB, P 8 KB; at R = 64 P's hi takes the place of the
-// tile's rope chunk, which is dead by then. Tiles are handed out chunk by
-// chunk (four of 128 dims and the rope): PV releases each chunk as it goes, so
-// the next but one tile loads under it.
+// tile's rope chunk, which is dead by then. A tile's place is handed out in two
+// halves (dims 0-255; 256-511 and the rope): PV releases each as it goes, so the
+// next but one tile loads under it.
 //
 // Work is split over SMs by tiles, not by sequences: the tiles of all items
 // (R rows of one sequence) form one list, and CTA c of G takes its c-th part.
 // An item that crosses CTAs leaves partial results in the workspace, which
 // cache_attn_combine joins. The list's length comes from the batch arrays, so
 // each CTA counts it for itself; nothing of it is needed on the host.
+//
+// What bounds it (B200, 1.9 GHz; times with the combine pass):
+//  - R = 64: 2,048 queries x 32 heads at 8,192 keys 1.09 ms (936 TFLOP/s), 8,192
+//    queries with a window of 2,048 + 16 keys 1.56 ms (753 TFLOP/s). The MMAs of
+//    a tile read 344 KB of operands at 128 bytes a clock, 2,690 clocks, of which
+//    their math is 2,180; a tile takes about 4,000. The difference is the
+//    turnaround of a tile's place: PV done, seen by the producer (about 600
+//    clocks: polls wait for the MMAs' reads), loaded (about 400), seen by the MMA
+//    warp. A third place would hide it and does not fit beside 72 KB of Q. An
+//    item begins with 8,000 clocks for its Q, partly under the last PV.
+//  - R = 32: 64 sequences of 1 to 17,408 rows 105 us (3.2 TB/s of cache bytes).
+//    QK^T (1,000 clocks), softmax (1,300) and PV (950) of a tile follow each
+//    other unless the next tile has landed in time; the loads alone would take
+//    3,300 clocks a tile at 6.5 TB/s. Skipping half of the loads changed the
+//    time by 2 %, L2 prefetches of later tiles made it 10 % longer.
+//  - one sequence of 17,408 rows 22.5 us: 16 us of the first kernel, most of it
+//    the chain schedule - Q - first tile - epilogue of cold loads, then the
+//    combine pass.
 #include <cuda_bf16.h>
 #include <limits.h>
 

@@ -460,6 +460,20 @@ def test_nothing_to_do(dsa):
     assert float(x.abs().max()) == 0.0
 
 
+def test_sequences_without_new_tokens_and_many_of_them(dsa):
+    """Nothing but sequences without tokens; then 1,500 sequences, most of them
+    so (more than a block has threads), in both calls."""
+    s = Setup([70, 40], [0, 0], seed=27, pad=3)
+    run_attn(dsa, s)
+    run_append(dsa, s, False, heads=2, with_q=False)
+    rng = np.random.default_rng(28)
+    lens = rng.integers(1, 40, 1500).tolist()
+    new = [int(rng.random() < 0.05) for _ in lens]
+    s = Setup(lens, new, page=16, seed=28)
+    run_attn(dsa, s)
+    run_append(dsa, s, True, heads=3)
+
+
 # --------------------------------------------------------------- used together
 
 def test_append_then_attend_then_gather_into_the_sparse_layer(dsa):
