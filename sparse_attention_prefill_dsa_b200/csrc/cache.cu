@@ -161,12 +161,10 @@ __device__ void append_page(const AppendArgs& a, int64_t slot) {
   const int p0 = r.len - r.n;            // the sequence's first new position
   const int64_t pg = p0 / PS + j;        // this CTA's page of the sequence
   if (pg * PS >= r.len) return;
-  const int page = page_of(a.batch, b, pg);
-  if (!page_ok(a.cache, page)) return;
+  const int page = page_of(a.batch, b, pg);  // (looked at after the rows: the loads overlap)
   const int base = static_cast<int>(pg) * PS;
   const int r0 = max(p0 - base, 0), r1 = min(r.len - base, PS);  // new rows of the page
   const int64_t tok = static_cast<int64_t>(r.tok0) + base - p0;  // token of row 0 (row r0 on is real)
-  const float old_scale = __ldg(a.cache.scale + page);
   if (threadIdx.x == 0) s_exp = kCacheMinExp;
 
   int need = kCacheMinExp;
@@ -189,6 +187,8 @@ __device__ void append_page(const AppendArgs& a, int64_t slot) {
     }
     need = max(need, need_exp_f32(__uint_as_float(top)));
   }
+  if (!page_ok(a.cache, page)) return;
+  const float old_scale = r0 > 0 ? __ldg(a.cache.scale + page) : 0.f;
   double2 rot[C::kPairs];
 #pragma unroll
   for (int u = 0; u < C::kPairs; ++u) {

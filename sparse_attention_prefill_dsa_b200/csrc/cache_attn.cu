@@ -1279,11 +1279,13 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, 1)
   if (tid == 0) {
     ms->status = ms->info = 0u;
     ms->abort_flag = 0;
-    for (int b = 0; b < C::kNumBars; ++b)
-      mbar_init(x.bar(b), b == kQFull || b == kOFree || b == kPFull ? C::kWarps : 1);
-    fence_barrier_init();
     prefetch_tmap(&ml);
     prefetch_tmap(&mr);
+  }
+  if (tid >= 32 && tid < 32 + C::kNumBars) {
+    const int b = tid - 32;
+    mbar_init(x.bar(b), b == kQFull || b == kOFree || b == kPFull ? C::kWarps : 1);
+    fence_barrier_init();
   }
   if (warp == C::kWarps + 1) tmem_alloc(&ms->tmem, 512);
   __syncthreads();  // the status word before schedule() may report
