@@ -402,7 +402,8 @@ def _ld(ld, x, dim, default):
     strides = x.stride()
     if strides[-1] != 1 and x.shape[-1] > 1:
         raise ValueError("rows have to be dense in their last dimension")
-    return strides[dim] if x.shape[dim] > 1 else default
+    # (a dimension of one may have any stride)
+    return default if strides[dim] == default or x.shape[dim] == 1 else strides[dim]
 
 
 def dsa_cache_workspace_size(cache, batch, n_heads: int) -> int:

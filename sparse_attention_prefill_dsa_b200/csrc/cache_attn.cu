@@ -29,9 +29,9 @@
 // where the bytes bound; R = 64 else (P's lo and hi passes onto one O, N = 64),
 // which shares the loads between twice as many rows. Shared memory: Q 36 or
 // 72 KB, two tiles of 72 KB, P 8 KB; at R = 64 P's hi takes the place of the
-// tile's rope chunk, which is dead by then. A tile's place is handed out in two
-// halves (dims 0-255; 256-511 and the rope): PV releases each as it goes, so the
-// next but one tile loads under it.
+// tile's rope chunk, which is dead by then. A tile's place is handed out in four
+// chunks of 128 dims (the rope with the last): PV releases each as it goes, so
+// the next but one tile loads under it.
 //
 // Work is split over SMs by tiles, not by sequences: the tiles of all items
 // (R rows of one sequence) form one list, and CTA c of G takes its c-th part.
@@ -258,10 +258,10 @@ static_assert(sizeof(Misc) <= 48, "misc");
 
 // mbarriers: what TMA and the tensor cores arrive on, and rare events.
 enum Bars {
-  kFull = 0,              // [2 stages][2 halves] a tile's dims 0-255, 256-511 and rope have landed
-  kEmpty = 4,             // [2][2] the PV is done with them
-  kSFull = 8,             // [2] QK^T of a tile is done
-  kPvDone = 10,           // PV of a tile is done
+  kFull = 0,              // [2 stages][4 chunks] a chunk has landed (the last with the rope)
+  kEmpty = 8,             // [2][4] the PV is done with it
+  kSFull = 16,            // [2] QK^T of a tile is done
+  kPvDone = 18,           // PV of a tile is done
   kQFull,                 // the segment's Q is written
   kOFree,                 // the segment's O has been read
   kPFull,                 // P of a tile is written (kPollP)
@@ -761,22 +761,20 @@ __device__ void producer(const Ctx<R>& x, const CUtensorMap* ml, const CUtensorM
     const int st = i & 1;
     unsigned char* dst = x.s() + Cfg<R>::kOffStage + st * kStageBytes;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      if (i >= 2 && ok) ok = x.wait(kEmpty + 2 * st + c, ((i >> 1) - 1) & 1, kSiteEmpty);
+    for (int c = 0; c < 4; ++c) {
+      if (i >= 2 && ok) ok = x.wait(kEmpty + 4 * st + c, ((i >> 1) - 1) & 1, kSiteEmpty);
       ok = __all_sync(0xffffffffu, ok);
       if (ok) {
         // (not before the place is free: until then the barrier may still be
         // waiting for what was loaded there last)
-        uint64_t* full = x.bar(kFull + 2 * st + c);
-        if (lane == 0) mbar_arrive_expect_tx(full, bytes * (c == 0 ? 256 : 256 + kDR));
+        uint64_t* full = x.bar(kFull + 4 * st + c);
+        if (lane == 0) mbar_arrive_expect_tx(full, bytes * (c < 3 ? 128 : 128 + kDR));
         __syncwarp();
         if (pg >= 0) {
-          unsigned char* at = dst + 2 * c * kChunkBytes + lane * ps * 128;
-          tma_load_3d(at, ml, c * 256, 0, pg, full);
-          tma_load_3d(at + kChunkBytes, ml, c * 256 + 128, 0, pg, full);
-          if (c == 1) tma_load_3d(dst + kRopeOff + lane * ps * kDR, mr, 0, 0, pg, full);
+          tma_load_3d(dst + c * kChunkBytes + lane * ps * 128, ml, c * 128, 0, pg, full);
+          if (c == 3) tma_load_3d(dst + kRopeOff + lane * ps * kDR, mr, 0, 0, pg, full);
         }
-        c_failed = c + 1;
+        c_failed = c + 1;  // chunks of this tile that were asked for
       } else if (c == 0) {
         c_failed = 0;
       }
@@ -790,10 +788,10 @@ __device__ void producer(const Ctx<R>& x, const CUtensorMap* ml, const CUtensorM
   }
   if (!ok && lane == 0) {
     // Let the copies in flight land before the block ends: tile i - 1 was
-    // begun up to half c_failed, the one before it in full.
-    for (int c = 0; c < 2; ++c)
+    // begun up to chunk c_failed, the one before it in full.
+    for (int c = 0; c < 4; ++c)
       for (int j = max(i - 3, 0); j < i; ++j)
-        if (j < i - 1 || c < c_failed) drain_wait(x.bar(kFull + 2 * (j & 1) + c), (j >> 1) & 1);
+        if (j < i - 1 || c < c_failed) drain_wait(x.bar(kFull + 4 * (j & 1) + c), (j >> 1) & 1);
   }
 }
 
@@ -850,7 +848,7 @@ __device__ void mma_issuer(const Ctx<R>& x) {
   for (;;) {
     bool pv = v < q && (q == n || q - v == 2 || left == 0);
     if (C::kPollP && !pv && v < q) {
-      const int r = ok ? wait_either(x.bar(kFull + 2 * (q & 1) + 1), (q >> 1) & 1, x.bar(kPFull),
+      const int r = ok ? wait_either(x.bar(kFull + 4 * (q & 1) + 3), (q >> 1) & 1, x.bar(kPFull),
                                      v & 1, x.ms(), kSiteP) : 0;
       ok = ok && r != 0;
       pv = r == 2;
@@ -879,7 +877,7 @@ __device__ void mma_issuer(const Ctx<R>& x) {
             for (int kk = 0; kk < 4; ++kk)
               mma_f8_ss(d, av + ((kk * 4096) >> 4), dp + ((kk * 2048) >> 4), C::kIdescPV, 1u);
           }
-          if (c & 1) mma_commit(x.bar(kEmpty + 2 * (i & 1) + c / 2));  // a half goes as its blocks are done
+          mma_commit(x.bar(kEmpty + 4 * (i & 1) + c));  // a chunk goes as its block is done
         }
         mma_commit(x.bar(kPvDone));
       }
@@ -899,16 +897,15 @@ __device__ void mma_issuer(const Ctx<R>& x) {
       const uint64_t so = static_cast<uint64_t>((i & 1) * kStageBytes) >> 4;
       const uint32_t d = C::kTmemS + 2 * R * (i & 1);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        ok = ok && x.wait(kFull + 2 * (i & 1) + c, (i >> 1) & 1, kSiteFull);
+      for (int c = 0; c < 4; ++c) {
+        ok = ok && x.wait(kFull + 4 * (i & 1) + c, (i >> 1) & 1, kSiteFull);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
         if (ok && lead) {
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            mma_f8_ss(d, dk + so + (((2 * c + ks / 4) * kChunkBytes + ks % 4 * 32) >> 4),
-                      dq + (((2 * c + ks / 4) * C::kQChunk + ks % 4 * 32) >> 4), C::kIdescQK,
-                      c > 0 || ks > 0);
+          for (int ks = 0; ks < 4; ++ks)
+            mma_f8_ss(d, dk + so + ((c * kChunkBytes + ks * 32) >> 4),
+                      dq + ((c * C::kQChunk + ks * 32) >> 4), C::kIdescQK, c > 0 || ks > 0);
         }
       }
       if (ok && lead) {
@@ -1240,7 +1237,7 @@ __device__ void softmax_warps(const Ctx<R>& x) {
         // have landed (QK^T read them); waiting on them orders the writes.
 #pragma unroll 1
         for (int c = g; c < 4; c += C::kGroups) {
-          const bool there = x.wait(kFull + 2 * (i & 1) + c / 2, (i >> 1) & 1, kSiteFull);
+          const bool there = x.wait(kFull + 4 * (i & 1) + c, (i >> 1) & 1, kSiteFull);
           if (gone && there) {
             // (lanes start at different units, for different banks)
 #pragma unroll
