@@ -765,11 +765,14 @@ __device__ void producer(const Ctx<R>& x, const CUtensorMap* ml, const CUtensorM
       if (i >= 2 && ok) ok = x.wait(kEmpty + 4 * st + c, ((i >> 1) - 1) & 1, kSiteEmpty);
       ok = __all_sync(0xffffffffu, ok);
       if (ok) {
-        // (not before the place is free: until then the barrier may still be
-        // waiting for what was loaded there last)
         uint64_t* full = x.bar(kFull + 4 * st + c);
-        if (lane == 0) mbar_arrive_expect_tx(full, bytes * (c < 3 ? 128 : 128 + kDR));
-        __syncwarp();
+        if (c == 0) {
+          // All four barriers are armed at once (each arrival costs a turn at
+          // shared memory). Not before the first chunk is free: until QK^T of
+          // the tile that was there is done they may still wait for its loads.
+          if (lane < 4) mbar_arrive_expect_tx(full + lane, bytes * (lane < 3 ? 128 : 128 + kDR));
+          __syncwarp();
+        }
         if (pg >= 0) {
           tma_load_3d(dst + c * kChunkBytes + lane * ps * 128, ml, c * 128, 0, pg, full);
           if (c == 3) tma_load_3d(dst + kRopeOff + lane * ps * kDR, mr, 0, 0, pg, full);
