@@ -40,19 +40,20 @@
 // each CTA counts it for itself; nothing of it is needed on the host.
 //
 // What bounds it (B200, 1.9 GHz; times with the combine pass):
-//  - R = 64: 2,048 queries x 32 heads at 8,192 keys 1.09 ms (936 TFLOP/s), 8,192
-//    queries with a window of 2,048 + 16 keys 1.56 ms (753 TFLOP/s). The MMAs of
+//  - R = 64: 2,048 queries x 32 heads at 8,192 keys 1.04 ms (987 TFLOP/s), 8,192
+//    queries with a window of 2,048 + 16 keys 1.54 ms (765 TFLOP/s). The MMAs of
 //    a tile read 344 KB of operands at 128 bytes a clock, 2,690 clocks, of which
-//    their math is 2,180; a tile takes about 4,000. The difference is the
+//    their math is 2,180; a tile takes about 3,800. The difference is the
 //    turnaround of a tile's place: PV done, seen by the producer (about 600
-//    clocks: polls wait for the MMAs' reads), loaded (about 400), seen by the MMA
-//    warp. A third place would hide it and does not fit beside 72 KB of Q. An
-//    item begins with 8,000 clocks for its Q, partly under the last PV.
-//  - R = 32: 64 sequences of 1 to 17,408 rows 105 us (3.2 TB/s of cache bytes).
-//    QK^T (1,000 clocks), softmax (1,300) and PV (950) of a tile follow each
-//    other unless the next tile has landed in time; the loads alone would take
-//    3,300 clocks a tile at 6.5 TB/s. Skipping half of the loads changed the
-//    time by 2 %, L2 prefetches of later tiles made it 10 % longer.
+//    clocks), loaded (about 400), seen by the MMA warp. A third place would hide
+//    it and does not fit beside 72 KB of Q. An item begins with 8,000 clocks for
+//    its Q, partly under the last PV.
+//  - R = 32: 64 sequences of 1 to 17,408 rows 107 us (3.1 TB/s of cache bytes;
+//    about 5 TB/s between the first tile and the last). QK^T (1,000 clocks),
+//    softmax (1,300) and PV (950) of a tile follow each other unless the next
+//    tile has landed in time; the loads alone would take 3,300 clocks a tile at
+//    6.5 TB/s. Skipping half of the loads changed the time by 2 %, L2 prefetches
+//    of later tiles made it 10 % longer.
 //  - one sequence of 17,408 rows 22.5 us: 16 us of the first kernel, most of it
 //    the chain schedule - Q - first tile - epilogue of cold loads, then the
 //    combine pass.
@@ -100,7 +101,6 @@ struct Item {
   int t_lo, t_hi;       // positions of the first and last row
   int win_lo, sink_hi;  // keys [win_lo, t_hi] and [0, sink_hi) are seen by some row
   int nst, wt0, nt;
-  __device__ __forceinline__ int tile(int k) const { return k < nst ? k : wt0 + k - nst; }
   __device__ __forceinline__ bool seen(int s) const {
     return s <= t_hi && (s >= win_lo || s < sink_hi);
   }
