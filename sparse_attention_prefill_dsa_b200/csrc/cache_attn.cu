@@ -5,13 +5,15 @@
 //
 // The (512, 64) shape runs on tcgen05 with the cache's own bytes as operands:
 // a tile of 128 keys goes from the pages to swizzled shared memory by TMA and
-// is never converted. kind::f8f6f4 multiplies e4m3 with e4m3, so the other
-// operand is split instead: q = qs * (hi + lo/16) and p = hi + lo with hi, lo
-// in e4m3. A bf16 q has 8 significant bits and e4m3 has 4, and the residual of
-// rounding 8 bits to 4 is a signed 4-bit number: hi + lo is q itself (down to
-// 2^-22 of the row's largest element, where lo leaves e4m3's range). For p the
-// residual is rounded once more, to 4 significant bits of its own: 2^-8 of p
-// at most, 7e-4 rms, where a bf16 p has 1.7e-3 rms.
+// is never converted. kind::f8f6f4 multiplies 8-bit types, so the other operand
+// is split instead: q = qs * (hi + lo/16) and p = hi + lo in two 8-bit parts. A
+// bf16 q has 8 significant bits and e4m3 has 4, and the residual of rounding 8
+// bits to 4 is a signed 4-bit number: hi + lo is q itself (down to 2^-22 of the
+// row's largest element, where lo leaves e4m3's range). For p the residual is
+// rounded once more: apart from hi (R = 32 below) to e4m3, to 2^-9 of p, 6e-4
+// rms; on hi's own accumulators (R = 64) to e5m2, to 2^-8 of p, 1.3e-3 rms, where
+// a bf16 p has 2^-8 and 1.6e-3 rms. Those bounds end at 2^-15 (2^-14) of the
+// row's reference, below.
 // Work of a tile, for R query rows (token, head) of one sequence:
 //   QK^T  S^T[key, (hi, lo) x row] = K . Q^T      M = 128 keys, N = 2R, K = 576
 //   softmax, one thread per key lane              p'' = 2^(z log2e + e_p - m)
@@ -19,11 +21,18 @@
 // V is the latent part of the K tile read MN-major. The page scales 2^e_p stay
 // out of the MMAs: in the logits they multiply S, in the output they are added
 // to p's exponent, and the row sum takes p'' 2^-e_p.
-// m is a running maximum of z log2e + e_p, lowered by 6: p'' starts at 2^6 at
-// most and m is raised only when a value passes 2^8 (e4m3 ends at 448); O is
-// rescaled in tensor memory then, by a power of two. A tile whose values stay
-// below needs no exchange between threads but one vote.
-//
+// m is a row's reference, an integer that keeps p'' where its parts are exact: it
+// is set so that the row's largest p'' of a tile is 2^5 to 2^6, raised when a
+// value passes 2^8 (e4m3 ends at 448), and lowered when all are below 1/2, so
+// that the flat tail behind one large weight (a first token's, say) does not
+// fall below the parts' last bits: with a reference that only rose, a row whose
+// first key has 0.8 of the weight of 17,000 was off by 40 %. O and l are rescaled
+// then, O in tensor memory, by a power of two. A tile whose values stay inside needs
+// no exchange between threads but one vote. That a row has fallen is noticed a
+// tile later (found before the tile's own products it cost 4.5 %, so 2 %), but
+// for a tile after a weight far above others, which is looked at in any case. So
+// a weight is off by 2^-8 of itself at most or, if that is more, by 2^-13
+// (R = 64) or 2^-14 of the largest in its tile or the one before.
 // Rows of a tile: R = 32 (P's hi and lo side by side as N = 64, O_hi and O_lo
 // apart) when no sequence can be expected to have more rows, as in decode,
 // where the bytes bound; R = 64 else (P's lo and hi passes onto one O, N = 64),
@@ -40,8 +49,8 @@
 // each CTA counts it for itself; nothing of it is needed on the host.
 //
 // What bounds it (B200, 1.9 GHz; times with the combine pass):
-//  - R = 64: 2,048 queries x 32 heads at 8,192 keys 1.04 ms (987 TFLOP/s), 8,192
-//    queries with a window of 2,048 + 16 keys 1.54 ms (765 TFLOP/s). The MMAs of
+//  - R = 64: 2,048 queries x 32 heads at 8,192 keys 1.06 ms (965 TFLOP/s), 8,192
+//    queries with a window of 2,048 + 16 keys 1.59 ms (741 TFLOP/s). The MMAs of
 //    a tile read 344 KB of operands at 128 bytes a clock, 2,690 clocks, of which
 //    their math is 2,180; a tile takes about 3,800. The difference is the
 //    turnaround of a tile's place: PV done, seen by the producer (about 600
@@ -313,6 +322,7 @@ struct Cfg {
   static constexpr int kSmemBytes = kOffMisc + kMiscBytes;
   static constexpr uint32_t kIdescQK = idesc_e4m3_f32(128, 2 * R);
   static constexpr uint32_t kIdescPV = idesc_e4m3_f32(128, 64, true, true);
+  static constexpr uint32_t kIdescPVLo = idesc_e4m3_f32(128, 64, true, true, true);  // P in e5m2
   static_assert(kOffStage % 1024 == 0 && kOffP % 1024 == 0, "operand alignment");
   static_assert(kSmemBytes <= 232448, "shared memory");
   static_assert(kTmemO + 256 <= 512, "tensor memory");
@@ -878,7 +888,7 @@ __device__ void mma_issuer(const Ctx<R>& x) {
           if constexpr (!C::kSplitO) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_f8_ss(d, av + ((kk * 4096) >> 4), dp + ((kk * 2048) >> 4), C::kIdescPV, 1u);
+              mma_f8_ss(d, av + ((kk * 4096) >> 4), dp + ((kk * 2048) >> 4), C::kIdescPVLo, 1u);
           }
           mma_commit(x.bar(kEmpty + 4 * (i & 1) + c));  // a chunk goes as its block is done
         }
@@ -968,6 +978,28 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+
+// The range of p'': at most 2^kTop, so that hi ends at 256 and its residual at 8.
+// A row's reference is raised when a weight of a tile would pass that, and
+// lowered when all its weights in a tile are below 2^kLow. It never goes more
+// than kReach below its highest: what comes later cannot matter then in float32,
+// and O, which is scaled up, stays far from float32's end. A weight 2^kFar above
+// another warp's largest, or above the reference, makes the next tile be looked at.
+constexpr float kTop = 8.f;
+constexpr float kLow = -1.f;
+constexpr float kReach = 40.f;
+constexpr float kFar = 6.f;
+constexpr float kLoScale = 32.f;
+
+// The codes of P's second part: residuals of hi. Apart from hi (R = 32) they are
+// e4m3, scaled; on hi's own accumulators (R = 64) there is no scale, and e5m2
+// reaches down to 2^-16, where e4m3 would end at 2^-9.
+template <bool kApart>
+__device__ __forceinline__ uint32_t p_low(float x, float y) {
+  return kApart ? f32_to_e4m3x2(x * kLoScale, y * kLoScale)
+                : __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E5M2);
+}
+
 // Softmax warps: warpgroup g takes the rows [16 g, 16 g + 16), a thread one key
 // lane (then one dim lane of O). Four groups at R = 64 rather than two with 32
 // rows each: twice the warps to hide the latencies of a tile's chain (load,
@@ -993,7 +1025,8 @@ __device__ void softmax_warps(const Ctx<R>& x) {
   int e_page = 0, t0 = 0;
   bool masked = false;
   float l[HR];
-  float m = 0.f;  // lane r: the reference of row 16 g + r, an integer
+  float m = 0.f;      // lane r: the reference of row 16 g + r, an integer
+  float m_top = 0.f;  // and the highest it has been
 #pragma unroll 1
   for (int seg = 0;; ++seg) {
     const bool more = seg == 0 || x.segment(seg - 1)->more != 0;
@@ -1054,7 +1087,7 @@ __device__ void softmax_warps(const Ctx<R>& x) {
             tmem_ld_wait();
 #pragma unroll
             for (int r = 0; r < HR; ++r)
-              o[r] = fmaf(__uint_as_float(w[r]), 0.0625f, __uint_as_float(v[r])) *
+              o[r] = fmaf(__uint_as_float(w[r]), 1.f / kLoScale, __uint_as_float(v[r])) *
                      __shfl_sync(0xffffffffu, inv, r);
           } else {
             tmem_ld_wait();
@@ -1101,6 +1134,14 @@ __device__ void softmax_warps(const Ctx<R>& x) {
     for (int r = 0; r < HR; ++r) l[r] = 0.f;
     m = 0.f;
     uint32_t unset = (1u << HR) - 1u;                      // rows that saw no key yet
+    // the item's rows of this group, row r as bit 6 of a code, by the byte and the
+    // register that its codes are in
+    uint32_t mine = 0u;
+#pragma unroll
+    for (int r = 0; r < HR; ++r)
+      mine |= r < x.segment(seg)->it.n_rows - g * HR ? 64u << 8 * (r & 3) >> (r >> 2) : 0u;
+    bool small = false;  // some row's weights of the tile before were small
+    bool look = false;
     const float fac = rowfac[g * HR + (lane & (HR - 1))];  // lane r: the factor of row 16 g + r
     if (i == 0) {
       named_sync(kSReady, C::kSync);  // (tile 0)
@@ -1157,7 +1198,12 @@ __device__ void softmax_warps(const Ctx<R>& x) {
       for (int r = 1; r < HR; ++r) over = fmaxf(over, y[r]);
       // the previous PV has to be waited for (a segment's last one was)
       bool pv_due = k > 0;
-      if (named_or(kVote + g, 128, over > 8.f) || unset != 0u) {
+      // A row's reference may have to move: one of its weights is above 2^kTop,
+      // they may all have been small in the tile before, or the tile before
+      // showed a weight far above others, so that they may be small now.
+      const bool shift = named_or(kVote + g, 128, over > kTop || small) || unset != 0u || look;
+      look = false;
+      if (shift) {
         // a new reference for the rows that need one
         float mx = -INFINITY;
 #pragma unroll
@@ -1167,17 +1213,29 @@ __device__ void softmax_warps(const Ctx<R>& x) {
         }
         if (lane < HR) my_m[lane] = mx;
         named_sync(kVote + g, 128);
+        float mn = INFINITY;  // the least of the four warps' maxima
         if (lane < HR) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) mx = fmaxf(mx, s_m[HR * (4 * g + q) + lane]);
+          for (int q = 0; q < 4; ++q) {
+            const float v = s_m[HR * (4 * g + q) + lane];
+            mx = fmaxf(mx, v);
+            mn = v == -INFINITY ? mn : fminf(mn, v);
+          }
         }
         named_sync(kVote + g, 128);
         const bool fresh = (unset >> lane) & 1u;
-        const bool up = lane < HR && (fresh ? mx > -INFINITY : mx > 8.f);
-        const float d = up ? ceilf(mx) - 6.f : 0.f;  // what the reference rises by
-        const float f = up && !fresh ? ex2_approx(-d) : 1.f;
-        unset &= ~__ballot_sync(0xffffffffu, up);
+        float d = 0.f;  // what the reference rises by
+        if (lane < HR && mx > -INFINITY) {
+          if (fresh) d = ceilf(mx) - 6.f;
+          else if (mx > kTop) d = ceilf(mx) - 6.f;
+          else if (mx < kLow) d = fminf(fmaxf(ceilf(mx) - 4.f, m_top - kReach - m), 0.f);
+        }
+        look = __any_sync(0xffffffffu, mx - mn > kFar || (!fresh && d > kFar));
+        const float f = fresh ? 1.f : ex2_approx(-d);
+        const bool seen = fresh && lane < HR && mx > -INFINITY;
+        unset &= ~__ballot_sync(0xffffffffu, seen);
         m += d;
+        m_top = seen ? m : fmaxf(m_top, m);
 #pragma unroll
         for (int r = 0; r < HR; ++r) y[r] -= __shfl_sync(0xffffffffu, d, r);
         if (__any_sync(0xffffffffu, f != 1.f)) {
@@ -1218,10 +1276,9 @@ __device__ void softmax_warps(const Ctx<R>& x) {
           }
           const uint32_t h0 = f32_to_e4m3x2(p[0], p[1]), h1 = f32_to_e4m3x2(p[2], p[3]);
           const float2 b0 = e4m3x2_to_f32(h0), b1 = e4m3x2_to_f32(h1);
-          constexpr float kLo = C::kSplitO ? 16.f : 1.f;
           hi[r / 4] = h0 | h1 << 16;
-          lo[r / 4] = f32_to_e4m3x2((p[0] - b0.x) * kLo, (p[1] - b0.y) * kLo) |
-                      f32_to_e4m3x2((p[2] - b1.x) * kLo, (p[3] - b1.y) * kLo) << 16;
+          lo[r / 4] = p_low<C::kSplitO>(p[0] - b0.x, p[1] - b0.y) |
+                      p_low<C::kSplitO>(p[2] - b1.x, p[3] - b1.y) << 16;
         }
       }
       if (pv_due) named_sync(kPvReady + ((i - 1) & 1), C::kSync);  // P's place is free
@@ -1263,6 +1320,16 @@ __device__ void softmax_warps(const Ctx<R>& x) {
         e_page = next->exp[slot];
         t0 = next->t0;
         masked = next->masked != 0;
+      }
+      if (quarter == 0 && k + 1 < n_seg) {
+        // For the next tile's vote: does some row have no weight of 2^kLow here
+        // (bit 6 of its codes, or bits 4 and 5)? Of the group's warps the first
+        // speaks for all; a row that is small there only costs the vote.
+        uint32_t some = 0u;
+#pragma unroll
+        for (int q = 0; q < HR / 4; ++q)
+          some |= ((hi[q] | (hi[q] << 1 & hi[q] << 2)) & 0x40404040u) >> q;
+        small = (~__reduce_or_sync(0xffffffffu, some) & mine) != 0u;
       }
     }
   }

@@ -178,12 +178,13 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn, b
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// Instruction descriptor of kind::f8f6f4 with e4m3 A and B (format code 0),
-// float32 D, both operands K-major unless the *_mn flags are set.
+// Instruction descriptor of kind::f8f6f4 with e4m3 A and e4m3 or e5m2 B (format
+// codes 0 and 1), float32 D, both operands K-major unless the *_mn flags are set.
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, bool a_mn = false,
-                                                      bool b_mn = false) {
-  return (1u << 4) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
-         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+                                                      bool b_mn = false, bool b_e5m2 = false) {
+  return (1u << 4) | (static_cast<uint32_t>(b_e5m2) << 10) | (static_cast<uint32_t>(a_mn) << 15) |
+         (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
 }
 
 // D[tmem] (+)= A[smem] * B[smem]^T, issued by one thread.
