@@ -538,6 +538,19 @@ dsa_status dsa_partition_queries(const dsa_dims* dims, int32_t n_parts, int32_t*
 dsa_status dsa_selftest_bounded_wait(void* workspace, size_t workspace_bytes, int64_t* cycles,
                                      void* stream);
 
+/* dsa_cache_attn at (512, 64) with every wait of its kernel limited to
+ * wait_cycles (>= 0) SM clock cycles, for a test of its failure path: a wait
+ * that is over in time changes nothing, and one that gives up ends the call
+ * with DSA_ERR_TIMEOUT in the workspace status, outputs unspecified. The
+ * kernel's blocks end and the context stays usable in either case. Arguments
+ * and errors as dsa_cache_attn (DSA_ERR_DIMS for wait_cycles < 0 and other
+ * shapes). */
+dsa_status dsa_selftest_cache_wait(const dsa_cache* cache, const dsa_batch* batch,
+                                   const uint16_t* q, int32_t n_heads, float softmax_scale,
+                                   int32_t window, int32_t n_sink, uint16_t* out, float* lse,
+                                   int64_t wait_cycles, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
 /* Start-up self-test of the tensor-core operand layouts the kernels use (the
  * TensorFold issue #743 page, "Pre-M5 kernel checks": a load-time check of the
  * matrix-fragment layout that a transposed operand got through). One CTA

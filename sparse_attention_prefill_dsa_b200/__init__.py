@@ -64,7 +64,7 @@ EXPORTED = ("dsa_workspace_size", "dsa_index_scores", "dsa_topk_select",
             "dsa_selftest_bounded_wait", "dsa_partition_queries", "dsa_sparse_attn_decode",
             "dsa_decode_layer", "dsa_sparse_attn_block", "dsa_quantize_fp8",
             "dsa_index_scores_fp8", "dsa_selftest_mma_layout", "dsa_cache_workspace_size",
-            "dsa_cache_append", "dsa_cache_gather", "dsa_cache_attn")
+            "dsa_cache_append", "dsa_cache_gather", "dsa_cache_attn", "dsa_selftest_cache_wait")
 
 
 class dsa_dims(ctypes.Structure):
@@ -168,6 +168,8 @@ def library():
     lib.dsa_cache_gather.argtypes = [_CP, _BP, i32, i32, i32, _P, _P, _P, size, _P]
     lib.dsa_cache_attn.argtypes = [_CP, _BP, _P, i32, ctypes.c_float, i32, i32, _P, _P, _P, size,
                                    _P]
+    lib.dsa_selftest_cache_wait.argtypes = [_CP, _BP, _P, i32, ctypes.c_float, i32, i32, _P, _P,
+                                            i64, _P, size, _P]
     lib.dsa_device_status.argtypes = [_P, _P]
     lib.dsa_status_string.argtypes = [ctypes.c_int32]
     lib.dsa_status_string.restype = ctypes.c_char_p
@@ -176,7 +178,7 @@ def library():
               "dsa_prefill_layer_host", "dsa_selftest_bounded_wait", "dsa_partition_queries",
               "dsa_sparse_attn_decode", "dsa_decode_layer", "dsa_sparse_attn_block",
               "dsa_quantize_fp8", "dsa_index_scores_fp8", "dsa_selftest_mma_layout",
-              "dsa_cache_append", "dsa_cache_gather", "dsa_cache_attn"):
+              "dsa_cache_append", "dsa_cache_gather", "dsa_cache_attn", "dsa_selftest_cache_wait"):
         getattr(lib, f).restype = ctypes.c_int32
     _lib = lib
     return lib
@@ -457,3 +459,12 @@ def dsa_cache_attn(cache, batch, q, n_heads, softmax_scale, window, n_sink, out,
     return library().dsa_cache_attn(cache, batch, _at(q), n_heads, softmax_scale, window, n_sink,
                                     _at(out), _at(lse), _at(workspace),
                                     _nbytes(workspace, workspace_bytes), _on(stream))
+
+
+def dsa_selftest_cache_wait(cache, batch, q, n_heads, softmax_scale, window, n_sink, out, lse,
+                            wait_cycles, workspace, workspace_bytes=None, stream=None) -> int:
+    """dsa_cache_attn with its waits limited to wait_cycles (see include/dsa.h)."""
+    return library().dsa_selftest_cache_wait(cache, batch, _at(q), n_heads, softmax_scale, window,
+                                             n_sink, _at(out), _at(lse), int(wait_cycles),
+                                             _at(workspace), _nbytes(workspace, workspace_bytes),
+                                             _on(stream))

@@ -128,6 +128,8 @@ cudaError_t launch_cache_gather(const dsa_cache& c, const dsa_batch& b, int seq,
                                 cudaStream_t st);
 // Workspace of the attention past the header.
 size_t cache_attn_scratch_bytes(const dsa_cache& c, const dsa_batch& b, int n_heads);
-cudaError_t launch_cache_attn(const CacheAttnArgs& a, void* scratch, cudaStream_t st);
+// wait_cycles: the limit of the kernel's waits where it is not negative (a test's).
+cudaError_t launch_cache_attn(const CacheAttnArgs& a, void* scratch, cudaStream_t st,
+                              long long wait_cycles = -1);
 
 }  // namespace dsa

@@ -76,6 +76,36 @@ dsa_status nothing_to_do(void* ws, void* stream) {
       cudaMemsetAsync(ws, 0, dsa::kWsHeaderBytes, static_cast<cudaStream_t>(stream)));
 }
 
+dsa_status attend(const dsa_cache* cache, const dsa_batch* batch, const uint16_t* q,
+                  int32_t n_heads, float softmax_scale, int32_t window, int32_t n_sink,
+                  uint16_t* out, float* lse, long long wait_cycles, void* workspace,
+                  size_t workspace_bytes, void* stream) {
+  dsa_status s = check_batch(cache, batch);
+  if (s != DSA_OK) return s;
+  if (n_heads < 1 || n_heads > 128 || window < 0 || n_sink < 0) return DSA_ERR_DIMS;
+  if (!(softmax_scale > 0.0f && softmax_scale < 1e30f)) return DSA_ERR_DIMS;
+  if (!q || !out) return DSA_ERR_NULL;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(lse)) return DSA_ERR_ALIGN;
+  s = check_ws(cache, batch, n_heads, false, workspace, workspace_bytes);
+  if (s != DSA_OK) return s;
+  s = check_device(workspace);
+  if (s != DSA_OK) return s;
+  if (batch->n_seq == 0 || batch->n_tok == 0) return nothing_to_do(workspace, stream);
+  dsa::CacheAttnArgs a;
+  a.cache = *cache;
+  a.batch = *batch;
+  a.q = q;
+  a.out = out;
+  a.lse = lse;
+  a.n_heads = n_heads;
+  a.window = window;
+  a.n_sink = n_sink;
+  a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  a.ws = static_cast<dsa::WsHeader*>(workspace);
+  return from_cuda(dsa::launch_cache_attn(a, static_cast<char*>(workspace) + dsa::kWsHeaderBytes,
+                                          static_cast<cudaStream_t>(stream), wait_cycles));
+}
+
 }  // namespace
 
 extern "C" {
@@ -152,30 +182,18 @@ dsa_status dsa_cache_attn(const dsa_cache* cache, const dsa_batch* batch, const 
                           int32_t n_heads, float softmax_scale, int32_t window, int32_t n_sink,
                           uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
                           void* stream) {
-  dsa_status s = check_batch(cache, batch);
-  if (s != DSA_OK) return s;
-  if (n_heads < 1 || n_heads > 128 || window < 0 || n_sink < 0) return DSA_ERR_DIMS;
-  if (!(softmax_scale > 0.0f && softmax_scale < 1e30f)) return DSA_ERR_DIMS;
-  if (!q || !out) return DSA_ERR_NULL;
-  if (!aligned16(q) || !aligned16(out) || !aligned16(lse)) return DSA_ERR_ALIGN;
-  s = check_ws(cache, batch, n_heads, false, workspace, workspace_bytes);
-  if (s != DSA_OK) return s;
-  s = check_device(workspace);
-  if (s != DSA_OK) return s;
-  if (batch->n_seq == 0 || batch->n_tok == 0) return nothing_to_do(workspace, stream);
-  dsa::CacheAttnArgs a;
-  a.cache = *cache;
-  a.batch = *batch;
-  a.q = q;
-  a.out = out;
-  a.lse = lse;
-  a.n_heads = n_heads;
-  a.window = window;
-  a.n_sink = n_sink;
-  a.scale_log2 = softmax_scale * 1.4426950408889634f;
-  a.ws = static_cast<dsa::WsHeader*>(workspace);
-  return from_cuda(dsa::launch_cache_attn(a, static_cast<char*>(workspace) + dsa::kWsHeaderBytes,
-                                          static_cast<cudaStream_t>(stream)));
+  return attend(cache, batch, q, n_heads, softmax_scale, window, n_sink, out, lse, -1, workspace,
+                workspace_bytes, stream);
+}
+
+dsa_status dsa_selftest_cache_wait(const dsa_cache* cache, const dsa_batch* batch,
+                                   const uint16_t* q, int32_t n_heads, float softmax_scale,
+                                   int32_t window, int32_t n_sink, uint16_t* out, float* lse,
+                                   int64_t wait_cycles, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+  if (wait_cycles < 0 || (cache && cache->d_latent != 512)) return DSA_ERR_DIMS;
+  return attend(cache, batch, q, n_heads, softmax_scale, window, n_sink, out, lse, wait_cycles,
+                workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

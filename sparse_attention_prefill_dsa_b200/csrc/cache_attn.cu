@@ -99,6 +99,7 @@ struct CacheAttnParams {
   CtaMeta* meta;   // [kMaxCtas]
   float2* part_ml; // [kMaxCtas][2][R]: (m, l)
   float* part_o;   // [kMaxCtas][2][R][kDC]
+  long long wait_cycles;  // limit of a wait
 };
 
 // R consecutive query rows of one sequence and the key tiles that any of them
@@ -331,6 +332,9 @@ struct Cfg {
 enum Sites { kSiteEmpty = 40, kSiteFull, kSiteSFull, kSitePv, kSiteQ, kSiteO, kSiteSeg, kSiteInfo, kSiteP };
 
 constexpr unsigned kPollPauseNs = 20;  // (0 to 100 measured alike)
+constexpr long long kPollCheckCycles = 1 << 20;  // waits shorter than this look at every poll
+// A steadfast wait (below) outlasts a chain of the MMA warp's own waits.
+constexpr long long kSteadfastCycles = 8 * kWaitLimitCycles;
 constexpr int kNoPage = 1 << 20;
 
 // The kernel's shared memory: a symbol, so that operand addresses are
@@ -620,15 +624,17 @@ __device__ void convert_q(const CacheAttnArgs& a, const Item& it, unsigned char*
 // The polling loop of a wait, once for all waits. Polls read shared memory,
 // which the MMAs keep busy: a warp that polls without a pause holds up the
 // others' (a producer that shared it with three such warps took 570 clocks for
-// each wait, barrier and load of a chunk).
-__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, Misc* ms, unsigned site) {
+// each wait, barrier and load of a chunk). It gives up after `limit` clocks, or
+// when another wait of the block has; a steadfast one only after its limit.
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, Misc* ms, unsigned site,
+                                     long long limit, bool steadfast) {
   const long long t0 = clock64();
   for (uint32_t i = 1;; ++i) {
     __nanosleep(kPollPauseNs);
     if (mbar_test_wait(bar, parity)) return true;
-    if ((i & 63u) == 0u) {
-      if (*reinterpret_cast<volatile int*>(&ms->abort_flag)) return false;
-      if (clock64() - t0 > kWaitLimitCycles) {
+    if ((i & 63u) == 0u || limit < kPollCheckCycles) {
+      if (!steadfast && *reinterpret_cast<volatile int*>(&ms->abort_flag)) return false;
+      if (clock64() - t0 > limit) {
         ms->abort_flag = 1;
         report(reinterpret_cast<WsHeader*>(&ms->status), kDevTimeout, site);
         return false;
@@ -654,7 +660,13 @@ struct Ctx {
     return reinterpret_cast<TileInfo*>(cache_attn_smem + Cfg<R>::kOffTile) + (i & 3);
   }
   __device__ __forceinline__ bool wait(int b, uint32_t parity, unsigned site) const {
-    return mbar_test_wait(bar(b), parity) || wait_on(bar(b), parity, ms(), site);
+    return mbar_test_wait(bar(b), parity) ||
+           wait_on(bar(b), parity, ms(), site, p.wait_cycles, false);
+  }
+  // For what comes also after a timeout, and keeps the warps in step.
+  __device__ __forceinline__ void wait_steadfast(int b, uint32_t parity, unsigned site) const {
+    if (!mbar_test_wait(bar(b), parity))
+      wait_on(bar(b), parity, ms(), site, kSteadfastCycles, true);
   }
   __device__ __forceinline__ bool wait_segment(int seg) const {
     return wait(kSeg + seg % kSegSlots, (seg / kSegSlots) & 1, kSiteSeg);
@@ -799,26 +811,30 @@ __device__ void producer(const Ctx<R>& x, const CUtensorMap* ml, const CUtensorM
     now = next;
     next = after;
   }
-  if (!ok && lane == 0) {
-    // Let the copies in flight land before the block ends: tile i - 1 was
-    // begun up to chunk c_failed, the one before it in full.
-    for (int c = 0; c < 4; ++c)
-      for (int j = max(i - 3, 0); j < i; ++j)
-        if (j < i - 1 || c < c_failed) drain_wait(x.bar(kFull + 4 * (j & 1) + c), (j >> 1) & 1);
+  if (lane == 0) {
+    // No copy may be in flight when the block ends, and after a timeout nobody
+    // else waits for the last ones. Tile i - 1 was begun up to chunk c_failed, the
+    // tile before it in full; the one before that landed if tile i - 1 was begun.
+    const int last = i - 1;
+    for (int c = 0; c < 4; ++c) {
+      const int j0 = c_failed == 0 ? max(last - 2, 0) : max(last - 1, 0);
+      const int j1 = c < c_failed ? last : last - 1;
+      for (int j = j0; j <= j1; ++j) drain_wait(x.bar(kFull + 4 * (j & 1) + c), (j >> 1) & 1);
+    }
   }
 }
 
 // Waits until one of two phases is complete: 1 or 2 (the first if both are), 0
 // after a timeout. The whole warp, one answer.
 __device__ __noinline__ int wait_either(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, Misc* ms,
-                                        unsigned site) {
+                                        unsigned site, long long limit) {
   const long long t0 = clock64();
   for (uint32_t i = 1;; ++i) {
     int r = mbar_test_wait(a, pa) ? 1 : mbar_test_wait(b, pb) ? 2 : 0;
     if (r == 0) __nanosleep(kPollPauseNs);
-    if (r == 0 && (i & 63u) == 0u) {
+    if (r == 0 && ((i & 63u) == 0u || limit < kPollCheckCycles)) {
       if (*reinterpret_cast<volatile int*>(&ms->abort_flag)) r = 3;
-      else if (clock64() - t0 > kWaitLimitCycles) {
+      else if (clock64() - t0 > limit) {
         ms->abort_flag = 1;
         report(reinterpret_cast<WsHeader*>(&ms->status), kDevTimeout, site);
         r = 3;
@@ -837,8 +853,11 @@ __device__ __noinline__ int wait_either(uint64_t* a, uint32_t pa, uint64_t* b, u
 // with it the load of the tile after, and a QK^T that waits for P would leave
 // the softmax without work. A segment's first QK^T comes after the last PV of
 // the one before, whose epilogue it overlaps.
-// After a timeout the warp goes on through the hardware barriers without
-// issuing.
+// After a timeout the warp goes on through all tiles without issuing, in step
+// with the softmax warps as before: it arrives itself where its commits would
+// have, so that the relays still tell the softmax of every product, in turn. (A
+// relay that went on by itself arrived twice at a hardware barrier before the
+// softmax had been there once, and some of its warps then waited for good.)
 template <int R>
 __device__ void mma_issuer(const Ctx<R>& x) {
   using C = Cfg<R>;
@@ -862,14 +881,14 @@ __device__ void mma_issuer(const Ctx<R>& x) {
     bool pv = v < q && (q == n || q - v == 2 || left == 0);
     if (C::kPollP && !pv && v < q) {
       const int r = ok ? wait_either(x.bar(kFull + 4 * (q & 1) + 3), (q >> 1) & 1, x.bar(kPFull),
-                                     v & 1, x.ms(), kSiteP) : 0;
+                                     v & 1, x.ms(), kSiteP, x.p.wait_cycles) : 0;
       ok = ok && r != 0;
       pv = r == 2;
     }
     if (pv) {
       const int i = v;
       const bool fresh = (first >> (i & 1)) & 1u;
-      if constexpr (C::kPollP) ok = ok && x.wait(kPFull, i & 1, kSiteP);
+      if constexpr (C::kPollP) x.wait_steadfast(kPFull, i & 1, kSiteP);
       else named_sync(kPReady, C::kSync);
       if (fresh && ++v_seg > 0) ok = ok && x.wait(kOFree, (v_seg - 1) & 1, kSiteO);
       ok = __all_sync(0xffffffffu, ok);
@@ -894,6 +913,7 @@ __device__ void mma_issuer(const Ctx<R>& x) {
         }
         mma_commit(x.bar(kPvDone));
       }
+      if (!ok && lead) mbar_arrive(x.bar(kPvDone));
       __syncwarp();
       if (++v == n) break;
     } else {
@@ -927,6 +947,7 @@ __device__ void mma_issuer(const Ctx<R>& x) {
           mma_f8_ss(d, dkr + so + ((ks * 32) >> 4), dqr + ((ks * 32) >> 4), C::kIdescQK, 1u);
         mma_commit(x.bar(kSFull + (i & 1)));
       }
+      if (!ok && lead) mbar_arrive(x.bar(kSFull + (i & 1)));
       __syncwarp();
       ++q;
       if (--left == 0) ++seg;
@@ -939,7 +960,7 @@ __device__ void mma_issuer(const Ctx<R>& x) {
 }
 
 // Relay warps: one sees S of every tile done, the other PV, and they tell the
-// softmax warps; after a timeout, too.
+// softmax warps. After a timeout the MMA warp still tells them of every tile.
 template <int R>
 __device__ void relay(const Ctx<R>& x, bool pv) {
   const int n = static_cast<int>(x.ms()->n_tiles);
@@ -947,11 +968,11 @@ __device__ void relay(const Ctx<R>& x, bool pv) {
 #pragma unroll 1
   for (int i = 0; i < n; ++i) {
     if (pv) {
-      ok = ok && x.wait(kPvDone, i & 1, kSitePv);
+      x.wait_steadfast(kPvDone, i & 1, kSitePv);
     } else {
       if (i == 0) ok = ok && x.wait(kInfo, 0, kSiteInfo);
       if (i + 1 < n) ok = ok && x.wait(kInfo + ((i + 1) & 3), ((i + 1) >> 2) & 1, kSiteInfo);
-      ok = ok && x.wait(kSFull + (i & 1), (i >> 1) & 1, kSiteSFull);
+      x.wait_steadfast(kSFull + (i & 1), (i >> 1) & 1, kSiteSFull);
     }
     named_arrive((pv ? kPvReady : kSReady) + (i & 1), Cfg<R>::kSync);
   }
@@ -1005,9 +1026,9 @@ __device__ __forceinline__ uint32_t p_low(float x, float y) {
 // rows each: twice the warps to hide the latencies of a tile's chain (load,
 // vote, exp2, conversions), in as many registers. The rows' references and
 // factors are in lanes and come by shuffles, not from shared memory.
-// These warps wait for nothing but the hardware barriers, which the relays
-// always reach: after a timeout all go through the barriers of every tile, and
-// nothing is stored.
+// These warps keep to the hardware barriers, which have no limit: the relays and
+// the MMA warp reach every one of them in the same order after a timeout too.
+// All then go through the barriers of every tile, and nothing is stored.
 template <int R>
 __device__ void softmax_warps(const Ctx<R>& x) {
   using C = Cfg<R>;
@@ -1124,7 +1145,12 @@ __device__ void softmax_warps(const Ctx<R>& x) {
       for (; i < n; ++i) {
         named_sync(kSReady + (i & 1), C::kSync);
         if (i + 2 < n) named_arrive(kSFree + (i & 1), C::kSync);
-        if constexpr (!C::kPollP) named_arrive(kPReady, C::kSync);
+        if constexpr (C::kPollP) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(x.bar(kPFull));
+        } else {
+          named_arrive(kPReady, C::kSync);
+        }
         named_sync(kPvReady + (i & 1), C::kSync);
       }
       break;
@@ -1694,7 +1720,8 @@ cudaError_t launch_rows(const CacheAttnArgs& a, cudaStream_t st) {
 }
 
 template <int R>
-cudaError_t launch_tc(const CacheAttnArgs& a, void* scratch, cudaStream_t st) {
+cudaError_t launch_tc(const CacheAttnArgs& a, void* scratch, long long wait_cycles,
+                      cudaStream_t st) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -1718,6 +1745,7 @@ cudaError_t launch_tc(const CacheAttnArgs& a, void* scratch, cudaStream_t st) {
   p.part_ml = reinterpret_cast<float2*>(w);
   w += kMaxCtas * 2 * R * sizeof(float2);
   p.part_o = reinterpret_cast<float*>(w);
+  p.wait_cycles = wait_cycles < 0 ? kWaitLimitCycles : wait_cycles;
   cache_attn_tc<R><<<grid, Cfg<R>::kThreads, Cfg<R>::kSmemBytes, st>>>(p, ml, mr);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -1727,12 +1755,13 @@ cudaError_t launch_tc(const CacheAttnArgs& a, void* scratch, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_cache_attn(const CacheAttnArgs& a, void* scratch, cudaStream_t st) {
+cudaError_t launch_cache_attn(const CacheAttnArgs& a, void* scratch, cudaStream_t st,
+                              long long wait_cycles) {
   if (a.cache.d_latent != kDC) return launch_rows(a, st);
   // R = 32 when the sequences have no more than 32 rows on average
   const int64_t rows = static_cast<int64_t>(a.batch.n_tok) * a.n_heads;
-  return rows <= 32ll * a.batch.n_seq ? launch_tc<32>(a, scratch, st)
-                                      : launch_tc<64>(a, scratch, st);
+  return rows <= 32ll * a.batch.n_seq ? launch_tc<32>(a, scratch, wait_cycles, st)
+                                      : launch_tc<64>(a, scratch, wait_cycles, st);
 }
 
 }  // namespace dsa
