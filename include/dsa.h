@@ -414,12 +414,15 @@ typedef struct dsa_cache {
  * page_size is skipped (its outputs are not written), a page outside
  * 0..n_pages-1 is skipped (its rows are not written, or not seen), and either
  * sets DSA_ERR_RANGE in the workspace status, as do cu_seqlens that do not
- * ascend within 0..n_tok: which sequences are skipped is not specified then. */
+ * ascend within 0..n_tok: which sequences are skipped is not specified then.
+ * With n_seq == 0 or n_tok == 0 the calls below launch no kernel and clear the
+ * status word; page_table and seq_lens (n_seq == 0) and the token tensors may
+ * be NULL then. */
 typedef struct dsa_batch {
   const int32_t* page_table; /* int32 [n_seq, max_pages]                               */
   const int32_t* cu_seqlens; /* int32 [n_seq + 1], ascending                           */
   const int32_t* seq_lens;   /* int32 [n_seq]                                          */
-  int32_t n_seq;             /* >= 0; 0 launches no kernel                             */
+  int32_t n_seq;             /* >= 0                                                   */
   int32_t max_pages;         /* >= 1                                                   */
   int32_t n_tok;             /* rows of the call's token tensors, >= 0                 */
   int32_t reserved;          /* 0                                                      */
@@ -471,7 +474,8 @@ dsa_status dsa_cache_append(const dsa_cache* cache, const dsa_batch* batch,
  * i.e. the latent and rope that the contiguous calls of this header take.
  * cu_seqlens and n_tok are not used. pos0 + n_rows <= seq_lens[seq] is checked
  * on the device (DSA_ERR_RANGE; rows past it, and rows of a page outside the
- * pool, are not written). n_rows == 0 launches no kernel.
+ * pool, are not written). n_rows == 0 launches no kernel, and latent and rope
+ * may be NULL then.
  * Errors: DSA_ERR_NULL, _ALIGN, _DIMS (a seq or range that cannot be),
  * _WORKSPACE, _DEVICE, _CUDA. */
 dsa_status dsa_cache_gather(const dsa_cache* cache, const dsa_batch* batch, int32_t seq,

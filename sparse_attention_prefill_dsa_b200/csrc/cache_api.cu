@@ -37,13 +37,16 @@ dsa_status check_sizes(const dsa_cache* c, const dsa_batch* b) {
 dsa_status check_batch(const dsa_cache* c, const dsa_batch* b) {
   const dsa_status s = check_sizes(c, b);
   if (s != DSA_OK) return s;
-  if (!c->latent || !c->rope || !c->scale || !b->page_table || !b->cu_seqlens || !b->seq_lens)
-    return DSA_ERR_NULL;
+  if (!c->latent || !c->rope || !c->scale || !b->cu_seqlens) return DSA_ERR_NULL;
+  if (b->n_seq > 0 && (!b->page_table || !b->seq_lens)) return DSA_ERR_NULL;
   if (!aligned16(c->latent) || !aligned16(c->rope) || !aligned16(c->scale) ||
       !aligned16(b->page_table) || !aligned16(b->cu_seqlens) || !aligned16(b->seq_lens))
     return DSA_ERR_ALIGN;
   return DSA_OK;
 }
+
+// Nothing to read or write: the token tensors may be NULL, as empty ones are.
+bool nothing(const dsa_batch* b) { return b->n_seq == 0 || b->n_tok == 0; }
 
 dsa_status check_ws(const dsa_cache* c, const dsa_batch* b, int32_t n_heads, bool header_only,
                     const void* ws, size_t bytes) {
@@ -84,13 +87,13 @@ dsa_status attend(const dsa_cache* cache, const dsa_batch* batch, const uint16_t
   if (s != DSA_OK) return s;
   if (n_heads < 1 || n_heads > 128 || window < 0 || n_sink < 0) return DSA_ERR_DIMS;
   if (!(softmax_scale > 0.0f && softmax_scale < 1e30f)) return DSA_ERR_DIMS;
-  if (!q || !out) return DSA_ERR_NULL;
+  if (!nothing(batch) && (!q || !out)) return DSA_ERR_NULL;
   if (!aligned16(q) || !aligned16(out) || !aligned16(lse)) return DSA_ERR_ALIGN;
   s = check_ws(cache, batch, n_heads, false, workspace, workspace_bytes);
   if (s != DSA_OK) return s;
   s = check_device(workspace);
   if (s != DSA_OK) return s;
-  if (batch->n_seq == 0 || batch->n_tok == 0) return nothing_to_do(workspace, stream);
+  if (nothing(batch)) return nothing_to_do(workspace, stream);
   dsa::CacheAttnArgs a;
   a.cache = *cache;
   a.batch = *batch;
@@ -124,7 +127,7 @@ dsa_status dsa_cache_append(const dsa_cache* cache, const dsa_batch* batch,
   dsa_status s = check_batch(cache, batch);
   if (s != DSA_OK) return s;
   if (rope_style != DSA_ROPE_INTERLEAVED && rope_style != DSA_ROPE_HALVES) return DSA_ERR_DIMS;
-  if (!latent || !rope || !inv_freq || !q_rope != !q) return DSA_ERR_NULL;
+  if (!inv_freq || (!nothing(batch) && (!latent || !rope || !q_rope != !q))) return DSA_ERR_NULL;
   if (!aligned16(latent) || !aligned16(rope) || !aligned16(inv_freq) || !aligned16(q_rope) ||
       !aligned16(q))
     return DSA_ERR_ALIGN;
@@ -138,7 +141,7 @@ dsa_status dsa_cache_append(const dsa_cache* cache, const dsa_batch* batch,
   if (s != DSA_OK) return s;
   s = check_device(workspace);
   if (s != DSA_OK) return s;
-  if (batch->n_seq == 0 || batch->n_tok == 0) return nothing_to_do(workspace, stream);
+  if (nothing(batch)) return nothing_to_do(workspace, stream);
   dsa::AppendArgs a;
   a.cache = *cache;
   a.batch = *batch;
@@ -166,7 +169,7 @@ dsa_status dsa_cache_gather(const dsa_cache* cache, const dsa_batch* batch, int3
       static_cast<int64_t>(pos0) + n_rows >
           static_cast<int64_t>(batch->max_pages) * cache->page_size)
     return DSA_ERR_DIMS;
-  if (!latent || !rope) return DSA_ERR_NULL;
+  if (n_rows > 0 && (!latent || !rope)) return DSA_ERR_NULL;
   if (!aligned16(latent) || !aligned16(rope)) return DSA_ERR_ALIGN;
   s = check_ws(cache, batch, 1, true, workspace, workspace_bytes);
   if (s != DSA_OK) return s;
