@@ -67,7 +67,6 @@
 //    the chain schedule - Q - first tile - epilogue of cold loads, then the
 //    combine pass.
 #include <cuda_bf16.h>
-#include <limits.h>
 
 #include "cache.cuh"
 #include "sm100_primitives.cuh"
@@ -731,22 +730,22 @@ __device__ void producer(const Ctx<R>& x, const CUtensorMap* ml, const CUtensorM
     sink_hi = sg.it.sink_hi;
   };
   enter();
-  // A tile's plan: this lane's page as the table has it (kNoPage when no row of
-  // the item sees any of it), its first key, whether all rows see all of it.
+  // A tile's plan: whether some row of the item sees any of this lane's page,
+  // the page as the table has it (any number), the tile's first key, whether all
+  // rows see all of it.
   const int page_shift = 31 - __clz(ps);
   struct Plan {
     int page, t0;
-    bool whole;
+    bool whole, wanted;
   };
   auto plan = [&] {
     Plan p;
     p.t0 = (k < nst ? k : wt0 + k - nst) * kKeys;
     p.whole = p.t0 + kKeys - 1 <= t_lo &&
               (a.window == 0 || p.t0 > t_hi - a.window || p.t0 + kKeys <= a.n_sink);
-    p.page = INT_MIN;
     const int s0 = p.t0 + lane * ps;
-    if (lane < npt && s0 <= t_hi && (s0 + ps > win_lo || s0 < sink_hi))
-      p.page = __ldg(table + (s0 >> page_shift));
+    p.wanted = lane < npt && s0 <= t_hi && (s0 + ps > win_lo || s0 < sink_hi);
+    p.page = p.wanted ? __ldg(table + (s0 >> page_shift)) : -1;
     if (++k == k1 && sg.next(a)) {
       enter();
       publish();
@@ -757,7 +756,7 @@ __device__ void producer(const Ctx<R>& x, const CUtensorMap* ml, const CUtensorM
   auto scale_of = [&](const Plan& p) { return in_pool(p.page) ? __ldg(a.cache.scale + p.page) : 0.f; };
   auto tell = [&](int i, const Plan& p, float sc) {
     const bool has = in_pool(p.page);
-    if (!has && p.page != INT_MIN) x.error(kCacheSitePage);
+    if (p.wanted && !has) x.error(kCacheSitePage);
     const bool full = __all_sync(0xffffffffu, has || lane >= npt) && p.whole;
     TileInfo* out = x.info(i);
     if (lane < npt) out->exp[lane] = has ? scale_exp(sc) : kNoPage;
