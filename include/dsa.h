@@ -109,7 +109,8 @@ typedef int32_t dsa_status;
 #define DSA_ERR_WORKSPACE (-5) /* workspace NULL or smaller than dsa_workspace_size()  */
 #define DSA_ERR_TIMEOUT (-6)   /* a device-side bounded wait gave up                   */
 #define DSA_ERR_CUDA (-7)      /* CUDA runtime or launch error                         */
-#define DSA_ERR_DEVICE (-8)    /* current device is not sm_100 (B200)                  */
+#define DSA_ERR_DEVICE (-8)    /* current device is not sm_100 (B200); paged cache: or the
+                                  workspace is not in its memory                       */
 #define DSA_ERR_RANGE (-9)     /* device found a selected index outside 0..t           */
 #define DSA_ERR_SCRATCH_LIMIT (-10) /* dsa_prefill_layer_noalloc: the chunk needs more
                                        scratch than DSA_NOALLOC_SCRATCH_BYTES             */

@@ -58,7 +58,8 @@ dsa_status check_ws(const dsa_cache* c, const dsa_batch* b, int32_t n_heads, boo
 }
 
 // The current device is a B200 and the one that holds the workspace (work on
-// another device's memory would run over NVLink, or fault).
+// another device's memory would run over NVLink, or fault, as it would on the
+// host's).
 dsa_status check_device(const void* ws) {
   const dsa_status s = dsa::check_current_device();
   if (s != DSA_OK) return s;
@@ -68,7 +69,8 @@ dsa_status check_device(const void* ws) {
     cudaGetLastError();
     return DSA_ERR_CUDA;
   }
-  return at.type == cudaMemoryTypeDevice && at.device != dev ? DSA_ERR_DEVICE : DSA_OK;
+  if (at.type == cudaMemoryTypeManaged) return DSA_OK;
+  return at.type == cudaMemoryTypeDevice && at.device == dev ? DSA_OK : DSA_ERR_DEVICE;
 }
 
 dsa_status from_cuda(cudaError_t e) { return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA; }

@@ -2,7 +2,7 @@
 import numpy as np
 import pytest
 
-from dsa_test_util import dev
+from dsa_test_util import dev, torch_mod
 from test_gpu_cache import Setup, dsa, run_attn  # noqa: F401 (a fixture)
 
 pytestmark = pytest.mark.gpu
@@ -15,3 +15,17 @@ def test_attn_reports_every_page_outside_the_pool(dsa, dc, heads, entry):  # noq
     s.table[1, 3] = entry  # rows 96..127
     s.d_table = dev(s.table)
     run_attn(dsa, s, want_status=dsa.DSA_ERR_RANGE)
+
+
+@pytest.mark.parametrize("pinned", [False, True])
+def test_a_workspace_in_host_memory_is_refused(dsa, pinned):  # noqa: F811
+    t = torch_mod()
+    s = Setup([70], [1], seed=4)
+    c, b = s.structs(dsa)
+    ws = t.zeros(dsa.dsa_cache_workspace_size(c, b, 32), dtype=t.uint8, pin_memory=pinned)
+    x = t.zeros(1, 32, 576, dtype=t.bfloat16, device="cuda")
+    freq = dev(s.inv_freq())
+    assert dsa.dsa_cache_attn(c, b, x, 32, 0.04, 0, 0, x, None, ws) == dsa.DSA_ERR_DEVICE
+    assert dsa.dsa_cache_append(c, b, x[:, 0], x[:, 0, :64], freq, 0, None, None, 1, ws,
+                                ld_latent=512, ld_rope=64) == dsa.DSA_ERR_DEVICE
+    assert dsa.dsa_cache_gather(c, b, 0, 0, 1, x, x, ws) == dsa.DSA_ERR_DEVICE
