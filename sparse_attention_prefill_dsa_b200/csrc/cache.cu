@@ -188,7 +188,8 @@ __device__ void append_page(const AppendArgs& a, int64_t slot) {
     need = max(need, need_exp_f32(__uint_as_float(top)));
   }
   if (!page_ok(a.cache, page)) return;
-  const float old_scale = r0 > 0 ? __ldg(a.cache.scale + page) : 0.f;
+  // (a plain load: thread 0 writes it below)
+  const float old_scale = r0 > 0 ? a.cache.scale[page] : 0.f;
   double2 rot[C::kPairs];
 #pragma unroll
   for (int u = 0; u < C::kPairs; ++u) {

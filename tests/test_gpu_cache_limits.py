@@ -2,8 +2,8 @@
 import numpy as np
 import pytest
 
-from dsa_test_util import dev, torch_mod
-from test_gpu_cache import Setup, dsa, run_attn  # noqa: F401 (a fixture)
+from dsa_test_util import dev, dev_bf16, torch_mod
+from test_gpu_cache import Setup, bf16, dsa, run_attn  # noqa: F401 (a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -29,3 +29,25 @@ def test_a_workspace_in_host_memory_is_refused(dsa, pinned):  # noqa: F811
     assert dsa.dsa_cache_append(c, b, x[:, 0], x[:, 0, :64], freq, 0, None, None, 1, ws,
                                 ld_latent=512, ld_rope=64) == dsa.DSA_ERR_DEVICE
     assert dsa.dsa_cache_gather(c, b, 0, 0, 1, x, x, ws) == dsa.DSA_ERR_DEVICE
+
+
+@pytest.mark.parametrize("page", [16, 64])
+def test_a_page_that_fills_token_by_token(dsa, page):  # noqa: F811
+    """Its scale is read, kept or raised, and written at every step."""
+    t = torch_mod()
+    s = Setup([page], [1], page=page, seed=page)
+    r, f = s.reference(), s.inv_freq()
+    c, _ = s.structs(dsa)
+    ws = t.empty(256, dtype=t.uint8, device="cuda")
+    for i in range(page):
+        lat_b, lat = bf16(s.rng.standard_normal((1, 512)) * 2.0 ** ((i * 7) % 11 + i // 4))
+        rope_b, rope = bf16(s.rng.standard_normal((1, 64)))
+        r.lens = np.array([i + 1], np.int32)
+        r.append(lat, rope, f, False)
+        b = dsa.make_batch(s.d_table, s.d_cu, dev(r.lens), 1)
+        dsa.check(dsa.dsa_cache_append(c, b, dev_bf16(lat_b), dev_bf16(rope_b), dev(f), 0, None, None,
+                                       1, ws))
+        dsa.check(dsa.dsa_device_status(ws))
+        np.testing.assert_array_equal(s.d_scale.cpu().numpy(), r.scale.astype(np.float32))
+        np.testing.assert_array_equal(s.d_latent.cpu().numpy(), r.latent)
+        np.testing.assert_array_equal(s.d_rope.cpu().numpy(), r.rope)
