@@ -373,6 +373,14 @@ __device__ __forceinline__ float warp_max(float x) {
   return y;
 }
 
+// log(2^m sum) for an integer m. The exponent of sum > 0 goes to m first: where
+// the pages' scales are far from 1 the two are large and of opposite sign.
+__device__ __forceinline__ float log_sum(float m, float sum) {
+  const uint32_t b = __float_as_uint(sum);
+  const float e = static_cast<float>(static_cast<int>(b >> 23) - 127);
+  return (m + e + log2f(__uint_as_float((b & 0x7FFFFFu) | 0x3F800000u))) * 0.69314718055994531f;
+}
+
 // Sum of v[e] over the 32 lanes for every e; lane l gets that of e = l % 16.
 __device__ __forceinline__ float warp_transpose_sum(float (&v)[16]) {
   const int lane = threadIdx.x & 31;
@@ -1087,7 +1095,7 @@ __device__ void softmax_warps(const Ctx<R>& x) {
         if (whole_item) {
           if (a.lse)
             a.lse[static_cast<int64_t>(it.row) + r0 + lane] =
-                sum > 0.f ? (m + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+                sum > 0.f ? log_sum(m, sum) : -INFINITY;
         } else {
           x.p.part_ml[part * R + r0 + lane] = make_float2(sum > 0.f ? m : -INFINITY, sum);
         }
@@ -1445,7 +1453,7 @@ struct RowParts {
   }
   __device__ __forceinline__ float inv() const { return sum > 0.f ? 1.f / sum : 0.f; }
   __device__ __forceinline__ float lse() const {
-    return sum > 0.f ? (mx + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+    return sum > 0.f ? log_sum(mx, sum) : -INFINITY;
   }
 };
 

@@ -2,8 +2,8 @@
 import numpy as np
 import pytest
 
-from dsa_test_util import dev, dev_bf16, torch_mod
-from test_gpu_cache import Setup, bf16, dsa, run_attn  # noqa: F401 (a fixture)
+from dsa_test_util import dev, dev_bf16, host_bf16_as_f32, torch_mod
+from test_gpu_cache import MARK, Setup, bf16, check_attn, dsa, run_attn  # noqa: F401 (a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +51,40 @@ def test_a_page_that_fills_token_by_token(dsa, page):  # noqa: F811
         np.testing.assert_array_equal(s.d_scale.cpu().numpy(), r.scale.astype(np.float32))
         np.testing.assert_array_equal(s.d_latent.cpu().numpy(), r.latent)
         np.testing.assert_array_equal(s.d_rope.cpu().numpy(), r.rope)
+
+
+def test_the_largest_values(dsa):  # noqa: F811
+    """The largest bf16 below 2^127 and a rotary pair whose turn comes as near: finite
+    through append, gather and attention. (Queries of 0: the logits are 0.)"""
+    t = torch_mod()
+    s = Setup([70], [70], page=64, seed=8)
+    r, f = s.reference(), s.inv_freq()
+    c, b = s.structs(dsa)
+    ws = s.workspace(dsa, c, b)
+    top = 2.0 ** 127 - 2.0 ** 119
+    lat_b, lat = bf16(np.where(s.rng.random((70, 512)) < 0.1, top, s.rng.standard_normal((70, 512))))
+    lat_b[:, ::7] ^= 0x8000
+    lat[:, ::7] *= -1
+    rope_b, rope = bf16(np.full((70, 64), top / 2))
+    r.append(lat, rope, f, False)
+    dsa.check(dsa.dsa_cache_append(c, b, dev_bf16(lat_b), dev_bf16(rope_b), dev(f), 0, None, None, 1,
+                                   ws))
+    dsa.check(dsa.dsa_device_status(ws))
+    assert r.scale[s.table[0, 0]] == 2.0 ** 119
+    np.testing.assert_array_equal(s.d_scale.cpu().numpy(), r.scale.astype(np.float32))
+    np.testing.assert_array_equal(s.d_latent.cpu().numpy(), r.latent)
+    np.testing.assert_array_equal(s.d_rope.cpu().numpy(), r.rope)
+    g_lat = t.empty(70, 512, dtype=t.bfloat16, device="cuda")
+    g_rope = t.empty(70, 64, dtype=t.bfloat16, device="cuda")
+    dsa.check(dsa.dsa_cache_gather(c, b, 0, 0, 70, g_lat, g_rope, ws))
+    want, _ = r.rows(0, np.arange(70))
+    assert np.isfinite(want).all() and np.abs(want).max() == 2.0 ** 127
+    np.testing.assert_array_equal(host_bf16_as_f32(g_lat), want[:, :512])
+    np.testing.assert_array_equal(host_bf16_as_f32(g_rope), want[:, 512:])
+    q = t.zeros(70, 32, 576, dtype=t.bfloat16, device="cuda")
+    out = t.full((70, 32, 512), MARK, dtype=t.bfloat16, device="cuda")
+    lse = t.full((70, 32), MARK, dtype=t.float32, device="cuda")
+    dsa.check(dsa.dsa_cache_attn(c, b, q, 32, 0.04, 0, 0, out, lse, ws))
+    dsa.check(dsa.dsa_device_status(ws))
+    check_attn(host_bf16_as_f32(out), lse.cpu().numpy(),
+               r.attend(np.zeros((70, 32, 576)), float(np.float32(0.04)), 0, 0))
