@@ -460,8 +460,12 @@ size_t dsa_cache_workspace_size(const dsa_cache* cache, const dsa_batch* batch, 
  *   q       bf16 [n_tok, n_heads, d_latent + d_rope] or NULL with q_rope: its
  *           last d_rope elements of each row receive the rotated q_rope (the
  *           rest is not touched): the q of dsa_cache_attn
- * The ld are multiples of 8, and their rows must not overlap in q.
- * No page may receive rows of two sequences. Inputs may not alias outputs.
+ * The ld are multiples of 8. Values must be finite and, rotated, below 2^127 in
+ * magnitude: code * scale is then finite as well. Others are not looked for: an
+ * infinity or NaN gives its page the largest scale, in which the page's other
+ * rows become 0, and NaN stays NaN.
+ * No page may receive rows of two sequences, or stand at two places of one
+ * sequence that receive rows. Inputs may not alias outputs.
  * Errors: DSA_ERR_NULL, _ALIGN (an ld too), _DIMS, _WORKSPACE, _DEVICE, _CUDA. */
 dsa_status dsa_cache_append(const dsa_cache* cache, const dsa_batch* batch,
                             const uint16_t* latent, int64_t ld_latent, const uint16_t* rope,
@@ -500,8 +504,8 @@ dsa_status dsa_cache_gather(const dsa_cache* cache, const dsa_batch* batch, int3
  *   q    bf16 [n_tok, n_heads, d_latent + d_rope], finite, rotated
  *   out  bf16 [n_tok, n_heads, d_latent] (output)
  *   lse  f32  [n_tok, n_heads] (output) or NULL
- * Visible rows must be finite (append writes no other codes); bytes of rows
- * that no token of the batch's sequence sees may be anything. The work of a
+ * Visible rows must be finite (append writes no other codes for finite values);
+ * bytes of rows that no token of the batch's sequence sees may be anything. The work of a
  * long sequence is spread over SMs, so sums may be grouped differently for
  * another batch or GPU; the same call gives the same bits.
  * Errors: DSA_ERR_NULL, _ALIGN, _DIMS, _WORKSPACE, _DEVICE, _CUDA. */
