@@ -88,3 +88,23 @@ def test_the_largest_values(dsa):  # noqa: F811
     dsa.check(dsa.dsa_device_status(ws))
     check_attn(host_bf16_as_f32(out), lse.cpu().numpy(),
                r.attend(np.zeros((70, 32, 576)), float(np.float32(0.04)), 0, 0))
+
+
+def test_statuses_of_calls_that_are_checked_together(dsa):  # noqa: F811
+    """Each call has the workspace of its own that the README gives it: what append
+    finds is there after the attention."""
+    t = torch_mod()
+    s = Setup([70, 40], [6, 1], page=32, seed=6)
+    s.lens[1] = 0  # a token, and no row for it
+    s.d_lens = dev(s.lens)
+    c, b = s.structs(dsa)
+    ws, ws2 = s.workspace(dsa, c, b), s.workspace(dsa, c, b)
+    x = t.zeros(7, 32, 576, dtype=t.bfloat16, device="cuda")
+    out = t.zeros(7, 32, 512, dtype=t.bfloat16, device="cuda")
+    dsa.check(dsa.dsa_cache_append(c, b, out[:, 0], x[:, 0, 512:], dev(s.inv_freq()), 0, None, None, 1,
+                                   ws))
+    sound = Setup([70, 40], [6, 1], page=32, seed=6)
+    c2, b2 = sound.structs(dsa)
+    dsa.check(dsa.dsa_cache_attn(c2, b2, x, 32, 0.04, 0, 0, out, None, ws2))
+    assert dsa.dsa_device_status(ws) == dsa.DSA_ERR_RANGE
+    assert dsa.dsa_device_status(ws2) == dsa.DSA_OK
