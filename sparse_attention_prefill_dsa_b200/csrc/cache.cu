@@ -40,9 +40,23 @@ __device__ void write_status(WsHeader* ws, unsigned int site) {
   if ((threadIdx.x & 31) == 0 && bad) atomicMax(&s_bad, bad);
   __syncthreads();
   if (threadIdx.x == 0) {
+#if defined(DSA_CHECK) && DSA_CHECK
+    if (s_bad) report(ws, kDevRange, s_bad);  // the word was cleared: others may have written it
+#else
     ws->status_info = s_bad;
     ws->status = s_bad ? kDevRange : 0u;
+#endif
   }
+}
+
+// Of the checking build, in which every block may report.
+cudaError_t clear_status_for_checks(WsHeader* ws, cudaStream_t st) {
+#if defined(DSA_CHECK) && DSA_CHECK
+  return cudaMemsetAsync(ws, 0, kWsHeaderBytes, st);
+#else
+  (void)ws, (void)st;
+  return cudaSuccess;
+#endif
 }
 
 __device__ __forceinline__ int page_of(const dsa_batch& bt, int seq, int64_t j) {
@@ -170,7 +184,7 @@ __device__ void append_page(const AppendArgs& a, int64_t slot) {
   int need = kCacheMinExp;
   auto unit = [&](int u) {
     const int x = threadIdx.x + u * C::kThr, row = x / C::kRowUnits;
-    return row >= r0 && row < r1
+    return row >= r0 && row < r1 && DSA_IN_BOUNDS(a.ws, tok + row, a.batch.n_tok, 60)
                ? __ldg(reinterpret_cast<const uint4*>(a.latent + (tok + row) * a.ld_latent) +
                        x % C::kRowUnits)
                : make_uint4(0u, 0u, 0u, 0u);
@@ -195,7 +209,7 @@ __device__ void append_page(const AppendArgs& a, int64_t slot) {
   for (int u = 0; u < C::kPairs; ++u) {
     const int x = threadIdx.x + u * C::kThr, row = x / C::kRowPairs, i = x % C::kRowPairs;
     rot[u] = make_double2(0.0, 0.0);
-    if (row >= r0 && row < r1) {
+    if (row >= r0 && row < r1 && DSA_IN_BOUNDS(a.ws, tok + row, a.batch.n_tok, 60)) {
       const uint16_t* src = a.rope + (tok + row) * a.ld_rope;
       const double v = bf16_to_f64(src[a.halves ? i : 2 * i]);
       const double w = bf16_to_f64(src[a.halves ? i + DR / 2 : 2 * i + 1]);
@@ -234,7 +248,7 @@ __device__ void append_page(const AppendArgs& a, int64_t slot) {
     uint2 v;
     v.x = f32_to_e4m3x2(f0.x * inv, f0.y * inv) | f32_to_e4m3x2(f1.x * inv, f1.y * inv) << 16;
     v.y = f32_to_e4m3x2(f2.x * inv, f2.y * inv) | f32_to_e4m3x2(f3.x * inv, f3.y * inv) << 16;
-    *reinterpret_cast<uint2*>(lat_page + x * 8) = v;
+    if (DSA_IN_BOUNDS(a.ws, x * 8 + 7, PS * DC, 61)) *reinterpret_cast<uint2*>(lat_page + x * 8) = v;
   }
   const double inv_d = static_cast<double>(inv);
 #pragma unroll
@@ -244,6 +258,7 @@ __device__ void append_page(const AppendArgs& a, int64_t slot) {
     const uint32_t v =
         f32_to_e4m3x2(f64_to_f32_odd(rot[u].x * inv_d), f64_to_f32_odd(rot[u].y * inv_d));
     uint8_t* dst = rope_page + row * DR;
+    if (!DSA_IN_BOUNDS(a.ws, row * DR + DR - 1, PS * DR, 62)) continue;
     if (a.halves) {
       dst[i] = static_cast<uint8_t>(v);
       dst[i + DR / 2] = static_cast<uint8_t>(v >> 8);
@@ -273,7 +288,9 @@ struct QItem {
     constexpr int kPerHead = DR / 16;
     const int g = x % kPerHead, h = (x / kPerHead) % a.n_heads, k = x / kPerHead / a.n_heads;
     const int64_t tok = tok0 + k;
-    if (tok >= a.batch.n_tok) return false;
+    if (tok >= a.batch.n_tok || !DSA_IN_BOUNDS(a.ws, tok * a.n_heads + h,
+                                               static_cast<int64_t>(a.batch.n_tok) * a.n_heads, 63))
+      return false;
     other = a.halves ? DR / 16 : 1;
     const int at = a.halves ? g : 2 * g;
     src = reinterpret_cast<const uint4*>(a.q_rope + tok * a.ld_q_tok + h * a.ld_q_head) + at;
@@ -452,7 +469,7 @@ __global__ void __launch_bounds__(GatherCfg<DC, DR>::kThr)
   uint16_t* out = lat ? a.latent + u * 16 : a.rope + (u - DC / 16) * 16;
 #pragma unroll
   for (int i = 0; i < C::kDeep; ++i) {
-    if (page[i] < 0) continue;
+    if (page[i] < 0 || !DSA_IN_BOUNDS(a.ws, row0 + i * C::kLanes, a.n_rows, 64)) continue;
     const float f = pow2f(scale_exp(s[i]));
     const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
     uint32_t o[8];
@@ -484,6 +501,8 @@ void launch_gather_t(const GatherArgs& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t st) {
+  const cudaError_t e = clear_status_for_checks(a.ws, st);
+  if (e != cudaSuccess) return e;
   return a.cache.d_latent == 512 ? launch_append_p<512, 64>(a, st)
                                  : launch_append_p<64, 16>(a, st);
 }
@@ -492,6 +511,8 @@ cudaError_t launch_cache_gather(const dsa_cache& c, const dsa_batch& b, int seq,
                                 int n_rows, uint16_t* latent, uint16_t* rope, WsHeader* ws,
                                 cudaStream_t st) {
   const bool wide = ((reinterpret_cast<uintptr_t>(latent) | reinterpret_cast<uintptr_t>(rope)) & 31u) == 0;
+  const cudaError_t e = clear_status_for_checks(ws, st);
+  if (e != cudaSuccess) return e;
   const GatherArgs a{c, b, latent, rope, seq, pos0, n_rows, wide, ws};
   if (c.d_latent == 512) launch_gather_t<512, 64>(a, st);
   else launch_gather_t<64, 16>(a, st);

@@ -322,7 +322,8 @@ struct Cfg {
   static constexpr int kSmemBytes = kOffMisc + kMiscBytes;
   static constexpr uint32_t kIdescQK = idesc_e4m3_f32(128, 2 * R);
   static constexpr uint32_t kIdescPV = idesc_e4m3_f32(128, 64, true, true);
-  static constexpr uint32_t kIdescPVLo = idesc_e4m3_f32(128, 64, true, true, true);  // P in e5m2
+  [[maybe_unused]] static constexpr uint32_t kIdescPVLo =
+      idesc_e4m3_f32(128, 64, true, true, true);  // P in e5m2
   static_assert(kOffStage % 1024 == 0 && kOffP % 1024 == 0, "operand alignment");
   static_assert(kSmemBytes <= 232448, "shared memory");
   static_assert(kTmemO + 256 <= 512, "tensor memory");
@@ -561,18 +562,31 @@ __device__ __forceinline__ uint32_t q_off(int n, int u) {
                       : 4 * Cfg<R>::kQChunk + n * 64 + (((u & 3) ^ ((n >> 1) & 3)) << 4);
 }
 
+// n rows from `row` on, or none where the checking build finds that they are not
+// all rows of the call.
+__device__ __forceinline__ int in_call(const CacheAttnArgs& a, int row, int n, WsHeader* ws,
+                                       unsigned int site) {
+  const int64_t rows = static_cast<int64_t>(a.batch.n_tok) * a.n_heads;
+  (void)rows;
+  return n <= 0 || (DSA_IN_BOUNDS(ws, row, rows, site) &&
+                    DSA_IN_BOUNDS(ws, static_cast<int64_t>(row) + n - 1, rows, site))
+             ? n
+             : 0;
+}
+
 // The item's rows as operand rows (hi at r, lo at R + r), their factors and
 // positions (less t_lo). Each softmax warp takes four rows: 144 units of 16
 // elements, five for a lane.
 template <int R>
 __device__ void convert_q(const CacheAttnArgs& a, const Item& it, unsigned char* sq, float* rowfac,
-                          uint8_t* row_dt) {
+                          uint8_t* row_dt, Misc* ms) {
+  WsHeader* ws = reinterpret_cast<WsHeader*>(&ms->status);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kUnits = (kDC + kDR) / 16;  // 36 of a row
   constexpr int kRows = 4, kRounds = (kRows * kUnits + 31) / 32;
   static_assert(R == kRows * Cfg<R>::kWarps, "rows of a warp");
   const uint4* src = reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(it.row) * (kDC + kDR));
-  const int r0 = warp * kRows, n_units = (min(it.n_rows, r0 + kRows) - r0) * kUnits;
+  const int r0 = warp * kRows, n_units = (min(in_call(a, it.row, it.n_rows, ws, 65), r0 + kRows) - r0) * kUnits;
   src += r0 * kUnits * 2;
   uint4 v[kRounds][2];
 #pragma unroll
@@ -1064,7 +1078,7 @@ __device__ void softmax_warps(const Ctx<R>& x) {
       // barrier: every warp is done with that one's factors)
       lost = named_or(kAll, 32 * C::kWarps, !x.wait_segment(seg));
       if (!lost) {
-        convert_q<R>(a, x.segment(seg)->it, x.s() + C::kOffQ, rowfac, row_dt);
+        convert_q<R>(a, x.segment(seg)->it, x.s() + C::kOffQ, rowfac, row_dt, x.ms());
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(x.bar(kQFull));
@@ -1089,7 +1103,9 @@ __device__ void softmax_warps(const Ctx<R>& x) {
       named_sync(kVote + g, 128);
       const int r0 = g * HR;
       const bool whole_item = sg.k0 == 0 && sg.k1 == it.nt;
-      const int n_rows = ok ? it.n_rows - r0 : 0;  // rows to store
+      // rows to store
+      const int n_rows = ok ? in_call(a, it.row + r0, min(it.n_rows - r0, HR),
+                                      reinterpret_cast<WsHeader*>(&x.ms()->status), 66) : 0;
       const int64_t part = 2ll * blockIdx.x + (sg.k0 == 0 ? 1 : 0);
       if (quarter == 0 && lane < HR && lane < n_rows) {
         if (whole_item) {
@@ -1472,6 +1488,14 @@ __device__ __forceinline__ void store_bf16x4(uint16_t* dst, const float4& v, flo
                                               *reinterpret_cast<const uint32_t*>(&hi));
 }
 
+// Rows of an item (last CTA, first CTA, row, rows) whose parts are to be joined;
+// none where the checking build finds a part or a row out of bounds.
+__device__ __forceinline__ int in_parts(const CacheAttnParams& p, const int4& me, unsigned int site) {
+  return DSA_IN_BOUNDS(p.a.ws, me.y, me.x + 1, site) && DSA_IN_BOUNDS(p.a.ws, me.x, kMaxCtas, site)
+             ? in_call(p.a, me.z, me.w, p.a.ws, site)
+             : 0;
+}
+
 // Joins the partial results of the items that cross CTAs: out = sum_c
 // 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c. An item in few parts (a batch: most
 // are in two) takes a warp for each row; one in many (a long sequence is in up
@@ -1510,10 +1534,12 @@ __global__ void __launch_bounds__(kCombineThreads)
       s_has[1][i] = many;
     }
   }
+#if !(defined(DSA_CHECK) && DSA_CHECK)  // (there other blocks may report; the host clears it)
   if (blockIdx.x == 0 && tid == 0) {
     p.a.ws->status = 0u;
     p.a.ws->status_info = 0u;
   }
+#endif
   __syncthreads();
   int n_few = 0, n_many = 0;
 #pragma unroll
@@ -1531,7 +1557,7 @@ __global__ void __launch_bounds__(kCombineThreads)
   for (int u = blockIdx.x * 4 + warp; u < n_few * R; u += gridDim.x * 4) {
     const int4 me = s_few[u / R];
     const int r = u % R, c0 = me.y, n = me.x - c0 + 1;
-    if (r >= me.w) continue;
+    if (r >= in_parts(p, me, 67)) continue;
     // (the item's first part is its CTA's second slot)
     auto part = [&](int j) { return (2ll * (c0 + j) + (j == 0 ? 1 : 0)) * R + r; };
     float4 v[kFewParts][4];
@@ -1560,7 +1586,7 @@ __global__ void __launch_bounds__(kCombineThreads)
   for (int u = blockIdx.x; u < n_many * R * 4; u += gridDim.x) {
     const int4 me = s_many[u / (4 * R)];
     const int r = (u >> 2) % R, quarter = u & 3, c0 = me.y, n = me.x - c0 + 1;
-    if (r >= me.w) continue;
+    if (r >= in_parts(p, me, 67)) continue;
     auto part = [&](int j) { return (2ll * (c0 + j) + (j == 0 ? 1 : 0)) * R + r; };
     // eight parts ahead, the first eight before the weights are known
     auto fetch = [&](float4(&v)[8], int j0) {
@@ -1626,6 +1652,7 @@ __global__ void __launch_bounds__(32 * kRowWarps)
   const SeqRange r = seq_range(a.batch, ps, b);
   if (r.n == 0) return;
   const int t = r.len - r.n + tok - r.tok0;
+  if (!DSA_IN_BOUNDS(a.ws, row, static_cast<int64_t>(a.batch.n_tok) * a.n_heads, 68)) return;
   const uint16_t* q = a.q + row * (DC + DR);
   for (int i = lane; i < DC + DR; i += 32) s_q[warp][i] = bf16_to_f32(q[i]) * a.scale_log2;
   __syncwarp();
@@ -1744,6 +1771,10 @@ cudaError_t launch_tc(const CacheAttnArgs& a, void* scratch, long long wait_cycl
                           CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
   const int grid = sms < kMaxCtas ? sms : kMaxCtas;
+#if defined(DSA_CHECK) && DSA_CHECK
+  e = cudaMemsetAsync(a.ws, 0, kWsHeaderBytes, st);
+  if (e != cudaSuccess) return e;
+#endif
   CacheAttnParams p;
   p.a = a;
   char* w = static_cast<char*>(scratch);
