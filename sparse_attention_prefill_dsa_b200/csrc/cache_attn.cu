@@ -322,8 +322,7 @@ struct Cfg {
   static constexpr int kSmemBytes = kOffMisc + kMiscBytes;
   static constexpr uint32_t kIdescQK = idesc_e4m3_f32(128, 2 * R);
   static constexpr uint32_t kIdescPV = idesc_e4m3_f32(128, 64, true, true);
-  [[maybe_unused]] static constexpr uint32_t kIdescPVLo =
-      idesc_e4m3_f32(128, 64, true, true, true);  // P in e5m2
+  static constexpr uint32_t kIdescPVLo = idesc_e4m3_f32(128, 64, true, true, !kSplitO);  // (e5m2)
   static_assert(kOffStage % 1024 == 0 && kOffP % 1024 == 0, "operand alignment");
   static_assert(kSmemBytes <= 232448, "shared memory");
   static_assert(kTmemO + 256 <= 512, "tensor memory");
@@ -925,7 +924,7 @@ __device__ void mma_issuer(const Ctx<R>& x) {
           for (int kk = 0; kk < 4; ++kk)
             mma_f8_ss(d, av + ((kk * 4096) >> 4), bh + ((kk * 2048) >> 4), C::kIdescPV,
                       kk > 0 ? 1u : fresh ? 0u : 1u);
-          if constexpr (!C::kSplitO) {
+          if (!C::kSplitO) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               mma_f8_ss(d, av + ((kk * 4096) >> 4), dp + ((kk * 2048) >> 4), C::kIdescPVLo, 1u);

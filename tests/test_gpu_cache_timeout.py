@@ -16,7 +16,7 @@ LIMITS = [1 << 31, 100000, 30000, 10000, 5000, 2500, 1200, 600, 300, 0]
 @pytest.mark.parametrize("window,n_sink", [(0, 0), (300, 20)])
 @pytest.mark.parametrize("lens,new,heads", [
     ([700], [1], 32),                 # 32 rows, a tile an SM
-    ([3000, 40, 900] * 60, [1] * 180, 32),  # 32 rows, several sequences an SM
+    ([3000, 40, 900] * 24, [1] * 72, 32),  # 32 rows, several sequences an SM
     ([900, 2500], [130, 700], 32)])   # 64 rows, several items an SM
 def test_waits_that_run_out_end_the_call(dsa, lens, new, heads, window, n_sink):  # noqa: F811
     t = torch_mod()

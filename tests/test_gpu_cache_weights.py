@@ -7,6 +7,8 @@ That bound counts 2^-8 of every weight. The keys that share a tile of 128 with t
 large one are held less exactly, to 2^-3 of themselves at worst: 127 roundings of
 weights that differ (their logits' sd is 0.5) average to less than 1 % of those
 keys' sum, of which the tail holds at least 16 times as much."""
+import functools
+
 import numpy as np
 import pytest
 
@@ -20,6 +22,19 @@ DC, DR = 512, 64
 SCALE = float(np.float32((DC + DR) ** -0.5))
 
 
+@functools.lru_cache(maxsize=1)
+def tail(n, page):
+    """Codes and scales of n rows of similar size, their rotary part 0."""
+    rng = np.random.default_rng(n)
+    pages = (n + page - 1) // page
+    some = rng.standard_normal((1024, DC)) + 0.5  # values that do not average out
+    x = np.zeros((pages * page, DC + DR))
+    x[:, :DC] = some[rng.integers(0, len(some), len(x))]
+    x = x.reshape(pages, page, DC + DR)
+    s = np.array([ref.need_scale(v) for v in np.abs(x).max((1, 2))])
+    return ref.encode(x / s[:, None, None]), s
+
+
 class Long:
     """One stored sequence of n rows with a large key at `at`, and n_seq batch
     entries that all refer to it, each with `new` tokens."""
@@ -29,17 +44,16 @@ class Long:
         self.n, self.at, self.heads, self.page = n, at, heads, page
         pages = (n + page - 1) // page
         self.n_pages = pages + 2
-        some = rng.standard_normal((1024, DC)) + 0.5  # values that do not average out
-        x = np.zeros((pages * page, DC + DR))
-        x[:, :DC] = some[rng.integers(0, len(some), len(x))]
+        codes, s = (x.copy() for x in tail(n, page))
         # The large key's logit comes from its rotary part, against queries whose
         # rotary part is 1. Its value is a tenth of the others' size.
         z = np.log(weight / (1 - weight)) + np.log(seen) + 0.125
-        x[at, :DC] *= 0.1
-        x[at, DC:] = z / (DR * SCALE)
-        x = x.reshape(pages, page, DC + DR)
-        s = np.array([ref.need_scale(v) for v in np.abs(x).max((1, 2))])
-        codes = ref.encode(x / s[:, None, None])
+        j = at // page
+        x = ref.VALUES[codes[j]] * s[j]
+        x[at % page, :DC] *= 0.1
+        x[at % page, DC:] = z / (DR * SCALE)
+        s[j] = ref.need_scale(np.abs(x).max())
+        codes[j] = ref.encode(x / s[j])
         order = rng.permutation(self.n_pages)[:pages]
         self.codes = np.full((self.n_pages, page, DC + DR), 0x7F, np.uint8)  # NaN elsewhere
         self.codes[order] = codes
