@@ -703,9 +703,14 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
     if (clock64() - t0 > kWaitLimitCycles) break;
 }
 
+// How far the producer came: its last tile, and the chunks that it asked for of it.
+struct Begun {
+  int tile, chunks;
+};
+
 // Producer warp: lane l < 128 / page_size loads the tile's l-th page.
 template <int R>
-__device__ void producer(const Ctx<R>& x, const CUtensorMap* ml, const CUtensorMap* mr) {
+__device__ Begun producer(const Ctx<R>& x, const CUtensorMap* ml, const CUtensorMap* mr) {
   const CacheAttnArgs& a = x.p.a;
   const int lane = threadIdx.x & 31, ps = a.cache.page_size, npt = kKeys / ps;
   const int n = static_cast<int>(x.ms()->n_tiles);
@@ -831,16 +836,18 @@ __device__ void producer(const Ctx<R>& x, const CUtensorMap* ml, const CUtensorM
     now = next;
     next = after;
   }
-  if (lane == 0) {
-    // No copy may be in flight when the block ends, and after a timeout nobody
-    // else waits for the last ones. Tile i - 1 was begun up to chunk c_failed, the
-    // tile before it in full; the one before that landed if tile i - 1 was begun.
-    const int last = i - 1;
-    for (int c = 0; c < 4; ++c) {
-      const int j0 = c_failed == 0 ? max(last - 2, 0) : max(last - 1, 0);
-      const int j1 = c < c_failed ? last : last - 1;
-      for (int j = j0; j <= j1; ++j) drain_wait(x.bar(kFull + 4 * (j & 1) + c), (j >> 1) & 1);
-    }
+  return {i - 1, c_failed};
+}
+
+// No copy may be in flight when the block ends, and after a timeout nobody else
+// waits for the last ones. Tile b.tile was begun up to chunk b.chunks, the tile
+// before it in full; the one before that landed if tile b.tile was begun.
+template <int R>
+__device__ __noinline__ void drain_copies(const Ctx<R>& x, const Begun b) {
+  for (int c = 0; c < 4; ++c) {
+    const int j0 = b.chunks == 0 ? max(b.tile - 2, 0) : max(b.tile - 1, 0);
+    const int j1 = c < b.chunks ? b.tile : b.tile - 1;
+    for (int j = j0; j <= j1; ++j) drain_wait(x.bar(kFull + 4 * (j & 1) + c), (j >> 1) & 1);
   }
 }
 
@@ -1413,9 +1420,10 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, 1)
     if (tid == 0) report(reinterpret_cast<WsHeader*>(&ms->status), kDevInternal, 0);
     work = false;
   }
+  Begun begun = {-1, 0};
   if (work) {
     if (warp < C::kWarps) softmax_warps<R>(x);
-    else if (warp == C::kWarps) producer<R>(x, &ml, &mr);
+    else if (warp == C::kWarps) begun = producer<R>(x, &ml, &mr);
     else if (warp == C::kWarps + 1) mma_issuer<R>(x);
     else relay<R>(x, warp == C::kWarps + 3);
   }
@@ -1425,6 +1433,7 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(ms->tmem, 512);
   }
+  if (begun.tile >= 0 && ms->abort_flag != 0 && (tid & 31) == 0) drain_copies<R>(x, begun);
   if (tid == 0) {
     CtaMeta& me = p.meta[blockIdx.x];
     me.status = ms->status;
