@@ -497,7 +497,7 @@ dsa_status dsa_cache_gather(const dsa_cache* cache, const dsa_batch* batch, int3
  * bf16 q and out, float32 logits, softmax sums and accumulation. In the sum
  * over the rows (not in lse) a weight is rounded: at (64, 16) to float32, at
  * (512, 64) to within 2^-8 of itself (as bf16 would) or, where that is more,
- * within 2^-13 of the largest weight in its tile of 128 keys (positions 128 j
+ * within 2^-11 of the largest weight in its tile of 128 keys (positions 128 j
  * to 128 j + 127) or the visible tile before, weights counted times their
  * pages' scales. A token
  * whose visible rows all lie in skipped pages gets out = 0 and lse = -inf.

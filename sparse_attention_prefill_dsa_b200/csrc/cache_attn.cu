@@ -23,7 +23,7 @@
 // to p's exponent, and the row sum takes p'' 2^-e_p.
 // m is a row's reference, an integer that keeps p'' where its parts are exact: it
 // is set so that the row's largest p'' of a tile is 2^5 to 2^6, raised when a
-// value passes 2^8 (e4m3 ends at 448), and lowered when all are below 1/2, so
+// value passes 2^8 (e4m3 ends at 448), and lowered when all are below 1/8, so
 // that the flat tail behind one large weight (a first token's, say) does not
 // fall below the parts' last bits: with a reference that only rose, a row whose
 // first key has 0.8 of the weight of 17,000 was off by 40 %. O and l are rescaled
@@ -31,8 +31,11 @@
 // no exchange between threads but one vote. That a row has fallen is noticed a
 // tile later (found before the tile's own products it cost 4.5 %, so 2 %), but
 // for a tile after a weight far above others, which is looked at in any case. So
-// a weight is off by 2^-8 of itself at most or, if that is more, by 2^-13
-// (R = 64) or 2^-14 of the largest in its tile or the one before.
+// a weight is off by 2^-8 of itself at most or, if that is more, by 2^-11
+// (R = 64) or 2^-12 of the largest in its tile or the one before. Logits that
+// differ more move it more often: 2,048 queries at 8,192 keys took 886 / 896 us
+// with the former reference and now at a standard deviation of 1, 895 / 930 at
+// 2, 894 / 1,029 at 3 (lowered below 1/2 already, 972 and 1,117).
 // Rows of a tile: R = 32 (P's hi and lo side by side as N = 64, O_hi and O_lo
 // apart) when no sequence can be expected to have more rows, as in decode,
 // where the bytes bound; R = 64 else (P's lo and hi passes onto one O, N = 64),
@@ -1034,9 +1037,9 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 // and O, which is scaled up, stays far from float32's end. A weight 2^kFar above
 // another warp's largest, or above the reference, makes the next tile be looked at.
 constexpr float kTop = 8.f;
-constexpr float kLow = -1.f;
+constexpr float kLow = -3.f;
 constexpr float kReach = 40.f;
-constexpr float kFar = 6.f;
+constexpr float kFar = 10.f;
 constexpr float kLoScale = 32.f;
 
 // The codes of P's second part: residuals of hi. Apart from hi (R = 32) they are
@@ -1378,12 +1381,12 @@ __device__ void softmax_warps(const Ctx<R>& x) {
       }
       if (quarter == 0 && k + 1 < n_seg) {
         // For the next tile's vote: does some row have no weight of 2^kLow here
-        // (bit 6 of its codes, or bits 4 and 5)? Of the group's warps the first
+        // (bits 5 and 6 of its codes)? Of the group's warps the first
         // speaks for all; a row that is small there only costs the vote.
         uint32_t some = 0u;
 #pragma unroll
         for (int q = 0; q < HR / 4; ++q)
-          some |= ((hi[q] | (hi[q] << 1 & hi[q] << 2)) & 0x40404040u) >> q;
+          some |= ((hi[q] | hi[q] << 1) & 0x40404040u) >> q;
         small = (~__reduce_or_sync(0xffffffffu, some) & mine) != 0u;
       }
     }

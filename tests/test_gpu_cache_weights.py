@@ -14,7 +14,7 @@ import pytest
 
 import cache_reference as ref
 from dsa_test_util import dev, dev_bf16, host_bf16_as_f32, torch_mod
-from test_gpu_cache import MARK, bf16, check_attn, dsa  # noqa: F401 (a fixture)
+from test_gpu_cache import MARK, Setup, bf16, check_attn, dsa, run_attn  # noqa: F401 (a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -149,3 +149,10 @@ def test_weights_that_fall_and_rise_again(dsa, n_seq, new):  # noqa: F811
             codes = ref.encode(np.nan_to_num(x) / s.scale[p])
         s.codes[p, :len(z)] = codes[:len(z)]
     s.run(dsa, 0, 0, 6)
+
+
+@pytest.mark.parametrize("scale", [0.08, 0.13, 0.3])
+@pytest.mark.parametrize("lens,new", [([2900, 700] * 8, [1, 1] * 8), ([2500, 900], [60, 70])])
+def test_logits_of_every_spread(dsa, lens, new, scale):  # noqa: F811
+    """Standard deviations of 2, 3 and 7: the references move up and down all the time."""
+    run_attn(dsa, Setup(lens, new, page=32, seed=int(100 * scale)), scale=scale)
